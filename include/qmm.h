@@ -312,6 +312,37 @@ int qmm_moe_gate_up_swiglu(const uint32_t* w_gate, const uint16_t* s_gate, const
 int qmm_moe_combine(const float* y_pairs, const float* weights, float* y, int t, int top_k, int n,
                     qmm_stream stream);
 
+/* Routing to experts: the step before qmm_moe_route and qmm_moe_combine.
+ * From router logits [T, E] fp32 (e.g. the output of qmm_qgemm over the
+ * router's weights), for every token t:
+ *   s[e] = softmax over e of logits[t, e]       (QMM_SCORE_SOFTMAX)
+ *        = 1 / (1 + exp(-logits[t, e]))         (QMM_SCORE_SIGMOID)
+ *   c[e] = s[e] + bias[e]                       (bias [E] fp32 or NULL)
+ *   the E experts form `groups` groups of E / groups neighbours; a group's
+ *       score is the sum of its group_top (1 or 2) largest c, and the
+ *       group_keep groups of the largest scores stay
+ *   expert_ids[t, :] = the top_k experts of those groups by c, largest first
+ *   weights[t, j] = scale * s[id_j] / (renormalize ? sum_j s[id_j] : 1)
+ * Equal values go to the lower index, of groups and of experts.  The choice is
+ * that of exact arithmetic: logits are compared as they are where only the
+ * order of the scores counts (no bias, group_top = 1), and s and c are
+ * formed in 64 bits otherwise.  The bias moves the choice, never the weights.
+ * A logit of -inf is an expert switched off: its score is 0 (it can still be
+ * returned, with weight 0, where top_k experts cannot be had otherwise or a
+ * bias lifts it).  A renormalizing sum of 0 (every chosen expert switched
+ * off) gives weights 0.  A token whose scores, choices or group scores hold
+ * a NaN (a NaN logit or bias; +inf under softmax) gets expert_ids
+ * 0 .. top_k-1 and NaN weights, so that the failure shows in its output.
+ *   groups: divides E, at most 64 (1: no groups, then group_keep = 1);
+ *   top_k: at most 64 and at most the experts of group_keep groups.
+ * One launch, no workspace.  t = 0 does nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED (score), HIP. */
+#define QMM_SCORE_SOFTMAX 0
+#define QMM_SCORE_SIGMOID 1
+int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, float* weights, int t,
+                 int e, int top_k, int score, int groups, int group_keep, int group_top,
+                 int renormalize, float scale, qmm_stream stream);
+
 /* ------------------------------------------------ load-time quantization
  * Asymmetric min/max quantization of a dense fp32 weight W[n, k] into the
  * packed format above: per group, s = fp16((max - min) / L) and

@@ -21,6 +21,7 @@ QMM_ERR_WORKSPACE = 3
 QMM_ERR_HIP = 4
 QMM_WEIGHTS_TILED = 0x100  # bits flag: weights from qmm_repack_tiled
 QMM_SCALES_TILED = 0x200  # bits flag: scales from qmm_repack_scales_tiled (biases unused)
+QMM_SCORE_SOFTMAX, QMM_SCORE_SIGMOID = 0, 1  # scores of qmm_moe_topk
 QMM_GROUPED_SCRATCH_BYTES = 1 << 20  # static scratch of qmm_qgemm_grouped_noalloc
 
 STATUS_NAMES = {0: "QMM_OK", 1: "QMM_ERR_INVALID_ARG", 2: "QMM_ERR_UNSUPPORTED",
@@ -44,7 +45,7 @@ class GemmProblem(C.Structure):
                 ("k", C.c_int32)]
 
 
-P, I, SZ = C.c_void_p, C.c_int, C.c_size_t
+P, I, SZ, F = C.c_void_p, C.c_int, C.c_size_t, C.c_float
 
 SIGNATURES = {
     "qmm_version": (I, []),
@@ -65,6 +66,7 @@ SIGNATURES = {
     "qmm_qgemm_grouped_routed": (I, [P, P, P, P, I, P, SZ, P, I, I, I, I, I, I, I, P]),
     "qmm_moe_gate_up_swiglu": (I, [P, P, P, P, P, P, P, P, SZ, P, I, I, I, I, I, I, I, P]),
     "qmm_moe_combine": (I, [P, P, P, I, I, I, P]),
+    "qmm_moe_topk": (I, [P, P, P, P, I, I, I, I, I, I, I, I, F, P]),
     "qmm_convert_bf16": (I, [P, P, SZ, P]),
     "qmm_repack_tiled": (I, [P, P, I, I, I, P]),
     "qmm_repack_scales_tiled": (I, [P, P, P, I, I, P]),

@@ -290,6 +290,52 @@ def moe_combine(y_pairs, weights, y=None, stream=None):
     return y
 
 
+_SCORES = {"softmax": _lib.QMM_SCORE_SOFTMAX, "sigmoid": _lib.QMM_SCORE_SIGMOID}
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    """Every tensor on one device, and that device current: the launch goes
+    there, whatever memory the pointers name."""
+    index = first.device.index
+    if index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.device.index != index:
+            raise ValueError(f"the tensors are on cuda:{index} and {t.device}")
+
+
+def moe_topk(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1,
+             group_keep: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+             expert_ids=None, weights=None, stream=None):
+    """(expert_ids int32 [T, top_k], weights fp32 [T, top_k]) of router logits
+    fp32 [T, E], via qmm_moe_topk: softmax or sigmoid scores, a bias [E] that
+    moves the choice only, the group_keep best of `groups` expert groups (by
+    the sum of their group_top largest choices), weights renormalized over the
+    chosen experts and scaled.  moe_route takes the ids, moe_combine the
+    weights."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], not {tuple(logits.shape)}")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {tuple(_SCORES)}, not {score!r}")
+    t, e = logits.shape
+    if bias is not None and bias.shape != (e,):
+        raise ValueError(f"bias must be [{e}], not {tuple(bias.shape)}")
+    if expert_ids is None:
+        expert_ids = torch.empty((t, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((t, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+    for out, name in ((expert_ids, "expert_ids"), (weights, "weights")):
+        if out.shape != (t, top_k):
+            raise ValueError(f"{name} must be [{t}, {top_k}], not {tuple(out.shape)}")
+    lp, ip, wp = _dev(logits, "logits", _Y), _dev(expert_ids, "expert_ids", (torch.int32,)), _dev(weights, "weights", _Y)
+    bp = None if bias is None else _dev(bias, "bias", _Y)
+    _same_device(logits, bias, expert_ids, weights)
+    check(lib().qmm_moe_topk(lp, bp, ip, wp, t, e, top_k, _SCORES[score], groups, group_keep, group_top,
+                             int(bool(renormalize)), scale, _stream(stream)))
+    return expert_ids, weights
+
+
 def convert_bf16(w_bf16, out=None, stream=None):
     """bf16 weights (torch.bfloat16, or int16 bit patterns) -> fp16 weights as
     int32 words [.., k/2] for bits = 16, via qmm_convert_bf16."""

@@ -569,6 +569,41 @@ int qmm_moe_combine(const float* y_pairs, const float* weights, float* y, int t,
   return hip_status(qmm::launch_moe_combine(y_pairs, weights, y, t, top_k, n, (hipStream_t)stream), fn);
 }
 
+int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, float* weights, int t,
+                 int e, int top_k, int score, int groups, int group_keep, int group_top,
+                 int renormalize, float scale, qmm_stream stream) {
+  const char* fn = "qmm_moe_topk";
+  clear_error();
+  if (t < 0) return fail(QMM_ERR_INVALID_ARG, "%s: t=%d must be >= 0", fn, t);
+  if (e < 1 || e > kMaxExperts)
+    return fail(QMM_ERR_INVALID_ARG, "%s: e=%d must be in [1, %d]", fn, e, kMaxExperts);
+  if (score != QMM_SCORE_SOFTMAX && score != QMM_SCORE_SIGMOID)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: score=%d not supported", fn, score);
+  if (groups < 1 || groups > qmm::kGroupsMax || e % groups != 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: groups=%d must be in [1, %d] and divide e=%d", fn, groups,
+                qmm::kGroupsMax, e);
+  if (group_keep < 1 || group_keep > groups)
+    return fail(QMM_ERR_INVALID_ARG, "%s: group_keep=%d must be in [1, groups=%d]", fn, group_keep, groups);
+  if (group_top < 1 || group_top > 2 || group_top > e / groups)
+    return fail(QMM_ERR_INVALID_ARG, "%s: group_top=%d must be 1 or 2 and at most e / groups = %d", fn,
+                group_top, e / groups);
+  const int eligible = e / groups * group_keep;
+  const int most = eligible < qmm::kTopkMax ? eligible : qmm::kTopkMax;
+  if (top_k < 1 || top_k > most)
+    return fail(QMM_ERR_INVALID_ARG, "%s: top_k=%d must be in [1, %d]", fn, top_k, most);
+  if (renormalize != 0 && renormalize != 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: renormalize must be 0 or 1", fn);
+  if (!(scale - scale == 0.0f)) return fail(QMM_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+  if (t == 0) return QMM_OK;
+  CHECK_PTR(logits, 4);
+  if (bias != nullptr) CHECK_PTR(bias, 4);
+  CHECK_PTR(expert_ids, 4);
+  CHECK_PTR(weights, 4);
+  const qmm::TopkArgs ta{logits, bias, expert_ids, weights, t, e, top_k, score, groups, group_keep,
+                         groups > 1 ? group_top : 1, renormalize, scale};
+  return hip_status(qmm::launch_moe_topk(ta, (hipStream_t)stream), fn);
+}
+
 int qmm_quantize(const float* w_f32, uint32_t* words, uint16_t* scales, uint16_t* biases,
                  int n, int k, int bits, int group_size, qmm_stream stream) {
   const char* fn = "qmm_quantize";

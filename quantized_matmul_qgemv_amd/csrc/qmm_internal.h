@@ -169,6 +169,22 @@ hipError_t launch_moe_swiglu(const uint32_t* wg, const uint16_t* sg, const uint1
 hipError_t launch_moe_combine(const float* y_pairs, const float* weights, float* y, int t, int top_k,
                               int n, hipStream_t st);
 
+// Choice of experts from router logits (moe_topk.hip).
+constexpr int kTopkMax = 64;    // experts per token: one lane each
+constexpr int kGroupsMax = 64;  // expert groups: one bit each
+struct TopkArgs {
+  const float* logits;  // [t, e]
+  const float* bias;    // [e] or null
+  int32_t* ids;         // [t, top_k]
+  float* weights;       // [t, top_k]
+  int t, e, top_k;
+  int score;  // 0: softmax, 1: sigmoid
+  int groups, group_keep, group_top;
+  int renormalize;
+  float scale;
+};
+hipError_t launch_moe_topk(const TopkArgs& a, hipStream_t st);
+
 hipError_t launch_quantize(const float* w, uint32_t* words, uint16_t* s, uint16_t* b, int n,
                            int k, int bits, int group_size, hipStream_t st);
 hipError_t launch_convert_bf16(const uint16_t* src, uint16_t* dst, long count, hipStream_t st);
