@@ -343,6 +343,59 @@ int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, fl
                  int e, int top_k, int score, int groups, int group_keep, int group_top,
                  int renormalize, float scale, qmm_stream stream);
 
+/* ----------------------------------------- low-rank adapters per request
+ * Many requests share a projection (qmm_qgemv, qmm_qgemm, the batched and
+ * the grouped products) and each has a low-rank adapter of its own:
+ *   y[p, :] = base[p, :] + scales[i] * B_s (A_s x[row(p), :]),   i = adapter_ids[p / top_k]
+ * for the rows p < t * top_k.
+ *   Dense projections: experts = 0, expert_ids NULL, top_k = 1; s = i.
+ *   Experts' products of a routed layer: pair p = token * top_k + j has
+ *       s = i * experts + expert_ids[p], the ids of qmm_moe_topk or
+ *       qmm_moe_route's input; row(p) = p with x_row_per_pair = 1 (the down
+ *       projection), p / top_k with 0 (gate, up).
+ *   x     fp16 bits, [t, k] or, with x_row_per_pair, [t * top_k, k]
+ *   a     fp16 bits, [adapters (x experts), rank, k]
+ *   b     fp16 bits, [adapters (x experts), n, rank]
+ *   base  fp32 [t * top_k, n], the shared product; it may be y itself (added
+ *         in place) or NULL (y is the adapters' part alone), but must not
+ *         overlap y otherwise
+ *   y     fp32 [t * top_k, n], overwritten
+ *   adapter_ids  [t] int32; -1: no adapter, the row is base (0 without base)
+ *   scales       [adapters] fp32 (alpha / rank), or NULL for 1
+ * An adapter id below -1 or >= adapters, or an expert id outside
+ * [0, experts) of a row with an adapter, makes the row NaN.
+ * The up to 8 problems of one call (q, k and v; gate and up) share the ids and
+ * run in the same launches; their y must not overlap.  Adapters of smaller
+ * rank are padded with zeros to the problem's rank, a multiple of 8 up to
+ * 256; k is a multiple of 64, adapters x experts at most 4096, n at most
+ * 2097152.  A B x is held in fp32 throughout (products of fp16, A x exact to
+ * 2^-23 of the row's largest value); non-finite adapter weights make
+ * non-finite outputs.  Results do not depend on scheduling, nor on what the
+ * other rows hold.
+ * Workspace: qmm_lora_workspace_size bytes for `rows` = t * top_k and `slots` =
+ * adapters * max(1, experts) (only k and rank of the problems are read; 0 for
+ * sizes that are refused), 16-byte aligned, contents on entry do not matter;
+ * calls (and captured graphs) that share one must not run concurrently.
+ * Up to 256 rows: two launches; more: one or two before them sort the rows by s.
+ * t = 0 does nothing.
+ * Errors: INVALID_ARG, WORKSPACE, HIP. */
+typedef struct {
+  const uint16_t* x;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* base;
+  float* y;
+  int32_t n;
+  int32_t k;
+  int32_t rank;
+  int32_t x_row_per_pair;
+} qmm_lora_problem;
+
+size_t qmm_lora_workspace_size(const qmm_lora_problem* problems, int count, int rows, int slots);
+int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter_ids,
+             const int32_t* expert_ids, const float* scales, int t, int top_k, int adapters,
+             int experts, void* workspace, size_t workspace_bytes, qmm_stream stream);
+
 /* ------------------------------------------------ load-time quantization
  * Asymmetric min/max quantization of a dense fp32 weight W[n, k] into the
  * packed format above: per group, s = fp16((max - min) / L) and

@@ -45,6 +45,12 @@ class GemmProblem(C.Structure):
                 ("k", C.c_int32)]
 
 
+class LoraProblem(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("a", C.c_void_p), ("b", C.c_void_p), ("base", C.c_void_p),
+                ("y", C.c_void_p), ("n", C.c_int32), ("k", C.c_int32), ("rank", C.c_int32),
+                ("x_row_per_pair", C.c_int32)]
+
+
 P, I, SZ, F = C.c_void_p, C.c_int, C.c_size_t, C.c_float
 
 SIGNATURES = {
@@ -67,6 +73,8 @@ SIGNATURES = {
     "qmm_moe_gate_up_swiglu": (I, [P, P, P, P, P, P, P, P, SZ, P, I, I, I, I, I, I, I, P]),
     "qmm_moe_combine": (I, [P, P, P, I, I, I, P]),
     "qmm_moe_topk": (I, [P, P, P, P, I, I, I, I, I, I, I, I, F, P]),
+    "qmm_lora_workspace_size": (SZ, [C.POINTER(LoraProblem), I, I, I]),
+    "qmm_lora": (I, [C.POINTER(LoraProblem), I, P, P, P, I, I, I, I, P, SZ, P]),
     "qmm_convert_bf16": (I, [P, P, SZ, P]),
     "qmm_repack_tiled": (I, [P, P, I, I, I, P]),
     "qmm_repack_scales_tiled": (I, [P, P, P, I, I, P]),

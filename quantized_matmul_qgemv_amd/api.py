@@ -16,7 +16,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import GemmProblem, GemvProblem, check, lib
+from ._lib import GemmProblem, GemvProblem, LoraProblem, check, lib
 
 GROUP = 64
 
@@ -334,6 +334,102 @@ def moe_topk(logits, top_k: int, bias=None, score: str = "softmax", groups: int 
     check(lib().qmm_moe_topk(lp, bp, ip, wp, t, e, top_k, _SCORES[score], groups, group_keep, group_top,
                              int(bool(renormalize)), scale, _stream(stream)))
     return expert_ids, weights
+
+
+def _lora_rows(problems, adapter_ids, expert_ids):
+    """(t, top_k, slots) of a call; every problem holds as many sets of weights."""
+    if not problems:
+        raise ValueError("no problems")
+    if adapter_ids.dim() != 1:
+        raise ValueError(f"adapter_ids must be [T], not {tuple(adapter_ids.shape)}")
+    t, top_k = adapter_ids.shape[0], 1
+    if expert_ids is not None:
+        if expert_ids.dim() != 2 or expert_ids.shape[0] != t:
+            raise ValueError(f"expert_ids must be [{t}, top_k], not {tuple(expert_ids.shape)}")
+        top_k = expert_ids.shape[1]
+    a = problems[0][1]
+    return t, top_k, a.numel() // (a.shape[-1] * a.shape[-2])
+
+
+def _lora_array(problems, t, top_k, slots, x_row_per_pair):
+    """The problems as the C ABI's array, their shapes checked against each other."""
+    arr = (LoraProblem * len(problems))()
+    for i, (x, a, b, base, y) in enumerate(problems):
+        rank, k, n = a.shape[-2], a.shape[-1], b.shape[-2]
+        want = (t * top_k if x_row_per_pair else t, k)
+        if x.shape != want:
+            raise ValueError(f"problem {i}: x must be {list(want)}, not {tuple(x.shape)}")
+        if a.numel() != slots * rank * k or b.shape[-1] != rank or b.numel() != slots * n * rank:
+            raise ValueError(f"problem {i}: a {tuple(a.shape)} and b {tuple(b.shape)} must be [{slots}, rank, k] "
+                             f"and [{slots}, n, rank]")
+        for o, name in ((base, "base"), (y, "y")):
+            if o is not None and o.shape != (t * top_k, n):
+                raise ValueError(f"problem {i}: {name} must be [{t * top_k}, {n}], not {tuple(o.shape)}")
+        arr[i] = LoraProblem(_dev(x, "x", _X), _dev(a, "a", _X), _dev(b, "b", _X),
+                             None if base is None else _dev(base, "base", _Y), _dev(y, "y", _Y), n, k, rank,
+                             int(bool(x_row_per_pair)))
+        _same_device(x, a, b, base, y)
+    return arr
+
+
+def lora_workspace(problems, adapter_ids, expert_ids=None):
+    """A workspace for lora and lora_batched calls of these sizes (kept by the
+    caller; calls that share one must not overlap in time)."""
+    t, top_k, slots = _lora_rows(problems, adapter_ids, expert_ids)
+    arr = (LoraProblem * len(problems))()
+    for i, (_, a, b, _, _) in enumerate(problems):
+        arr[i] = LoraProblem(None, None, None, None, None, b.shape[-2], a.shape[-1], a.shape[-2], 0)
+    need = lib().qmm_lora_workspace_size(arr, len(problems), t * top_k, slots)
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=adapter_ids.device)
+
+
+def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_pair: bool = False,
+                 workspace=None, stream=None):
+    """y = base + scales[id] * B_id (A_id x) for the projections of one input
+    (q, k and v; gate and up) in the same launches, via qmm_lora: a list of
+    (x, a, b, base, y) with base None or y itself to add in place.
+    adapter_ids int32 [T], -1 for no adapter; a [adapters, rank, k] and
+    b [adapters, n, rank] fp16.  With expert_ids [T, top_k] the rows are the
+    pairs of a routed layer and each adapter has weights for every expert
+    ([adapters, experts, ...], or flattened with scales given).  Returns the
+    list of y."""
+    t, top_k, slots = _lora_rows(problems, adapter_ids, expert_ids)
+    a = problems[0][1]
+    experts = 0
+    if expert_ids is not None:
+        if a.dim() == 4:
+            experts = a.shape[1]
+        elif scales is not None and scales.numel() > 0:
+            experts = slots // scales.numel()
+        else:
+            raise ValueError("a must be [adapters, experts, rank, k] (or scales [adapters] be given)")
+    adapters = slots // max(1, experts)
+    if adapters * max(1, experts) != slots:
+        raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
+    if scales is not None and scales.shape != (adapters,):
+        raise ValueError(f"scales must be [{adapters}], not {tuple(scales.shape)}")
+    problems = [p if p[4] is not None else (*p[:4], torch.empty(
+        (t * top_k, p[2].shape[-2]), dtype=torch.float32, device=p[0].device)) for p in problems]
+    arr = _lora_array(problems, t, top_k, slots, x_row_per_pair)
+    ip = _dev(adapter_ids, "adapter_ids", (torch.int32,))
+    ep = None if expert_ids is None else _dev(expert_ids, "expert_ids", (torch.int32,))
+    sp = None if scales is None else _dev(scales, "scales", _Y)
+    if workspace is None:
+        workspace = lora_workspace(problems, adapter_ids, expert_ids)
+    wp = _dev(workspace, "workspace", (torch.uint8,))
+    _same_device(problems[0][0], adapter_ids, expert_ids, scales, workspace)
+    check(lib().qmm_lora(arr, len(problems), ip, ep, sp, t, top_k, adapters, experts, wp, workspace.numel(),
+                         _stream(stream)))
+    return [p[4] for p in problems]
+
+
+def lora(x, a, b, adapter_ids, scales=None, base=None, y=None, expert_ids=None,
+         x_row_per_pair: bool = False, workspace=None, stream=None):
+    """y [rows, n] = base + scales[id] * B_id (A_id x) with each row's own
+    adapter, via qmm_lora (one problem; see lora_batched).  base None: the
+    adapters' part alone; base = y: added in place."""
+    return lora_batched([(x, a, b, base, y)], adapter_ids, scales, expert_ids, x_row_per_pair, workspace,
+                        stream)[0]
 
 
 def convert_bf16(w_bf16, out=None, stream=None):

@@ -80,6 +80,23 @@ int check_plan_size(const char* fn, size_t plan_bytes, int t, int top_k, int e) 
   return QMM_OK;
 }
 
+// Rows of one adapter call: pairs of a routed layer as in qmm_moe_route.
+constexpr long kMaxLoraRows = 0x7FFFFFFFL / 4;
+constexpr int kMaxLoraN = 1 << 21;  // column blocks of 64 in one grid dimension
+
+int check_lora_sizes(const char* fn, const qmm_lora_problem& q, int i) {
+  if (q.n < 1 || q.n > kMaxLoraN)
+    return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: n=%d must be in [1, %d]", fn, i, q.n, kMaxLoraN);
+  if (q.k < 64 || q.k % 64 != 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: k=%d must be a positive multiple of 64", fn, i, q.k);
+  if (q.rank < 8 || q.rank > qmm::kLoraMaxRank || q.rank % 8 != 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: rank=%d must be a multiple of 8 in [8, %d]", fn, i,
+                q.rank, qmm::kLoraMaxRank);
+  if (q.x_row_per_pair != 0 && q.x_row_per_pair != 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: x_row_per_pair must be 0 or 1", fn, i);
+  return QMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -602,6 +619,87 @@ int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, fl
   const qmm::TopkArgs ta{logits, bias, expert_ids, weights, t, e, top_k, score, groups, group_keep,
                          groups > 1 ? group_top : 1, renormalize, scale};
   return hip_status(qmm::launch_moe_topk(ta, (hipStream_t)stream), fn);
+}
+
+size_t qmm_lora_workspace_size(const qmm_lora_problem* problems, int count, int rows, int slots) {
+  if (problems == nullptr || count < 1 || count > qmm::kLoraMaxProblems) return 0;
+  if (rows < 1 || rows > kMaxLoraRows || slots < 1 || slots > qmm::kLoraMaxSlots) return 0;
+  qmm::LoraArgs g{};
+  g.count = count;
+  g.rows = rows;
+  g.slots = slots;
+  for (int i = 0; i < count; ++i) {
+    if (check_lora_sizes("", problems[i], i)) return 0;
+    g.p[i].k = problems[i].k;
+    g.p[i].rank = problems[i].rank;
+  }
+  return qmm::lora_layout(g);
+}
+
+int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter_ids,
+             const int32_t* expert_ids, const float* scales, int t, int top_k, int adapters,
+             int experts, void* workspace, size_t workspace_bytes, qmm_stream stream) {
+  const char* fn = "qmm_lora";
+  clear_error();
+  if (problems == nullptr) return fail(QMM_ERR_INVALID_ARG, "%s: null problems", fn);
+  if (count < 1 || count > qmm::kLoraMaxProblems)
+    return fail(QMM_ERR_INVALID_ARG, "%s: count=%d must be in [1, %d]", fn, count, qmm::kLoraMaxProblems);
+  if (t < 0) return fail(QMM_ERR_INVALID_ARG, "%s: t=%d must be >= 0", fn, t);
+  if (top_k < 1) return fail(QMM_ERR_INVALID_ARG, "%s: top_k=%d must be >= 1", fn, top_k);
+  if (adapters < 1) return fail(QMM_ERR_INVALID_ARG, "%s: adapters=%d must be >= 1", fn, adapters);
+  if (experts < 0) return fail(QMM_ERR_INVALID_ARG, "%s: experts=%d must be >= 0", fn, experts);
+  if (experts == 0 && top_k != 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: top_k=%d without experts must be 1", fn, top_k);
+  const long slots = (long)adapters * (experts > 0 ? experts : 1);
+  if (slots > qmm::kLoraMaxSlots)
+    return fail(QMM_ERR_INVALID_ARG, "%s: %ld sets of adapter weights, at most %d", fn, slots, qmm::kLoraMaxSlots);
+  if ((long)t * top_k > kMaxLoraRows) return fail(QMM_ERR_INVALID_ARG, "%s: too many rows", fn);
+  for (int i = 0; i < count; ++i)
+    if (int st = check_lora_sizes(fn, problems[i], i)) return st;
+  if (t == 0) return QMM_OK;
+  CHECK_PTR(adapter_ids, 4);
+  if (experts > 0) CHECK_PTR(expert_ids, 4);
+  if (scales != nullptr) CHECK_PTR(scales, 4);
+  qmm::LoraArgs g{};
+  for (int i = 0; i < count; ++i) {
+    const qmm_lora_problem& q = problems[i];
+    if (!q.x || !q.a || !q.b || !q.y)
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d has a null pointer", fn, i);
+    if (!aligned(q.x, 16) || !aligned(q.a, 16) || !aligned(q.b, 16))
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: x, a or b is not 16-byte aligned", fn, i);
+    if (!aligned(q.y, 4) || !aligned(q.base, 4))
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: base or y is not 4-byte aligned", fn, i);
+    const uintptr_t y = (uintptr_t)q.y, b = (uintptr_t)q.base;
+    const size_t bytes = (size_t)t * top_k * q.n * 4;
+    if (q.base != nullptr && y != b && y < b + bytes && b < y + bytes)
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: y overlaps base without being base", fn, i);
+    qmm::LoraProblem& p = g.p[i];
+    p.x = q.x;
+    p.a = q.a;
+    p.b = q.b;
+    p.base = q.base;
+    p.y = q.y;
+    p.n = q.n;
+    p.k = q.k;
+    p.rank = q.rank;
+    p.x_row_per_pair = q.x_row_per_pair;
+  }
+  g.count = count;
+  g.rows = t * top_k;
+  g.top_k = top_k;
+  g.adapters = adapters;
+  g.experts = experts > 0 ? experts : 1;
+  g.slots = (int)slots;
+  g.adapter_ids = adapter_ids;
+  g.expert_ids = experts > 0 ? expert_ids : nullptr;
+  g.scales = scales;
+  const size_t need = qmm::lora_layout(g);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
+  CHECK_PTR(workspace, 16);
+  g.v = static_cast<float*>(workspace);
+  g.plan = static_cast<int32_t*>(workspace);
+  return hip_status(qmm::launch_lora(g, (hipStream_t)stream), fn);
 }
 
 int qmm_quantize(const float* w_f32, uint32_t* words, uint16_t* scales, uint16_t* biases,

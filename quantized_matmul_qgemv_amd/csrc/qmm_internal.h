@@ -185,6 +185,41 @@ struct TopkArgs {
 };
 hipError_t launch_moe_topk(const TopkArgs& a, hipStream_t st);
 
+// Low-rank adapters (lora.hip).
+constexpr int kLoraMaxProblems = 8;
+constexpr int kLoraMaxSlots = 4096;     // adapters x experts: one LDS counter each
+constexpr int kLoraMaxRank = 256;
+constexpr int kLoraDirectRows = 256;    // rows up to which every workgroup finds its tile itself
+constexpr int kLoraTileRows = 64;       // rows of a sorted tile
+constexpr int kLoraPlanHeader = 8;      // words before the sorted rows
+constexpr int kLoraCountWords = 65536;  // chunks x buckets at most
+constexpr int kLoraChunkMin = 1024;     // rows a chunk at least
+constexpr int kLoraOneChunk = 4096;     // rows up to which one workgroup sorts all
+struct LoraProblem {
+  const uint16_t* x;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* base;
+  float* y;
+  int32_t n, k, rank, x_row_per_pair;
+  int32_t splits, k_per_split, rank_pad;
+  size_t v_offset;  // floats from the workspace's start: v [splits][rows][rank_pad]
+};
+struct LoraArgs {
+  LoraProblem p[kLoraMaxProblems];
+  const int32_t* adapter_ids;  // [rows / top_k]
+  const int32_t* expert_ids;   // [rows] or null
+  const float* scales;         // [adapters] or null
+  float* v;                    // the workspace, as floats
+  int32_t* plan;               // the workspace, as words: header, sorted rows, tiles, counts
+  size_t plan_tiles, plan_counts;
+  int32_t count, rows, top_k, adapters, experts, slots;
+  int32_t direct, chunk, chunks;
+  int64_t tiles;  // most tiles that the rows can form
+};
+size_t lora_layout(LoraArgs& g);
+hipError_t launch_lora(const LoraArgs& g, hipStream_t st);
+
 hipError_t launch_quantize(const float* w, uint32_t* words, uint16_t* s, uint16_t* b, int n,
                            int k, int bits, int group_size, hipStream_t st);
 hipError_t launch_convert_bf16(const uint16_t* src, uint16_t* dst, long count, hipStream_t st);
