@@ -19,7 +19,7 @@
 
 namespace qmm {
 
-constexpr int kTopkWaves = 4;  // tokens per workgroup, one per wave
+constexpr int kTopkWaves = 4;  // tokens per workgroup where a token has a whole wave
 
 // The larger choice of two, the lower index where they are equal; index -1
 // is no choice at all.
@@ -52,15 +52,14 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// One wave per token; lane i holds experts i, i + 64, ... (V of them).
+// ---------------------------------------------------------------- exact row
+// One token by a whole wave, in 64 bits: lane i holds experts i, i + 64, ...
+// (V of them), and top_k rounds of a maximum over the wave pick the experts.
+// `choices`: e doubles of LDS of this wave's own (used with groups).
 template <int V>
-__global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_kernel(TopkArgs a) {
-  extern __shared__ double choices[];  // [kTopkWaves][e], with groups only
+__device__ void exact_row(const TopkArgs& a, long tok, double* choices) {
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const long tok = (long)blockIdx.x * kTopkWaves + wave;
-  const bool live = tok < a.t;
-  const float* row = a.logits + (live ? tok : 0) * a.e;
+  const float* row = a.logits + tok * a.e;
   const bool by_logit = a.bias == nullptr && a.group_top == 1;
 
   float l[V];
@@ -90,27 +89,25 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_kernel(TopkArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = i * 64 + lane;
-    if (e >= a.e) {
-      c[i] = 0.0;
-      continue;
-    }
+    c[i] = 0.0;
+    if (e >= a.e) continue;
     alive |= 1u << i;
     c[i] = by_logit ? (double)l[i] : score(l[i]) + (a.bias ? (double)a.bias[e] : 0.0);
     bad |= c[i] != c[i];
   }
 
   if (a.groups > 1) {
-    double* mine = choices + (size_t)wave * a.e;
     const int size = a.e / a.groups;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i * 64 + lane < a.e) mine[i * 64 + lane] = c[i];
-    __syncthreads();
+      if (i * 64 + lane < a.e) choices[i * 64 + lane] = c[i];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();  // the wave's own LDS: writes before reads
     double g = 0.0;
     if (lane < a.groups) {
       double first = -__builtin_inf(), second = -__builtin_inf();
       for (int j = 0; j < size; ++j) {
-        const double v = mine[lane * size + j];
+        const double v = choices[lane * size + j];
         if (v > first) {
           second = first;
           first = v;
@@ -121,6 +118,7 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_kernel(TopkArgs a) {
       g = a.group_top == 1 ? first : first + second;
       bad |= g != g;
     }
+    __builtin_amdgcn_wave_barrier();
     int own = lane < a.groups ? lane : -1;
     uint64_t keep = 0;
     for (int j = 0; j < a.group_keep; ++j) {
@@ -156,7 +154,6 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_kernel(TopkArgs a) {
     if (lane == j) id = eb;
     if ((eb & 63) == lane) alive &= ~(1u << (eb >> 6));
   }
-  if (!live) return;
 
   const bool mine = lane < a.top_k;
   const float v = mine && !bad ? row[id] : -__builtin_inff();
@@ -177,15 +174,334 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_kernel(TopkArgs a) {
   }
 }
 
-hipError_t launch_moe_topk(const TopkArgs& a, hipStream_t st) {
+template <int V>
+__global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_wave_kernel(TopkArgs a) {
+  extern __shared__ double choices[];  // [kTopkWaves][e], with groups only
+  const int wave = threadIdx.x >> 6;
+  const long tok = (long)blockIdx.x * kTopkWaves + wave;
+  if (tok < a.t) exact_row<V>(a, tok, choices + (size_t)wave * a.e);
+}
+
+// ------------------------------------------------------------- sixteen lanes
+// One token by 16 lanes, four tokens a wave; lane i holds the `per` experts
+// from i * per on.
+//
+// A choice is packed with its expert into one 64-bit number that orders like
+// the choice and, where choices are equal, by the lower expert: a double in
+// [1, 2) whose mantissa holds 32 bits that order like the fp32 choice and 10
+// bits of 1023 - expert.  Comparing, then, is v_max_f64 / v_min_f64.  Each
+// lane sorts its experts down to a list of K (K >= top_k) with bitonic
+// networks, and four exchanges along the DPP row (neighbours, pairs, quads,
+// halves) merge the lists: max(a[i], b[K-1-i]) are the K largest of two
+// sorted lists, one more bitonic pass sorts them.
+//
+// Where the scores themselves are compared (SCORED) this runs on fp32 scores,
+// whose error is at most 2^-21 + 2^-23 |c| (exp2 and rcp to one unit, the
+// rounded argument: |l| s (1 - s) < 0.28), and is right unless two choices
+// that matter are nearer than twice that: neighbours among the chosen, the
+// last chosen and any other, a kept group and a dropped one.  Such rows, and
+// rows with a NaN, an infinite sum or nothing but -inf, go to exact_row.
+constexpr int kRowTokens = 16;  // tokens per workgroup of 256
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t r = (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u);
+  return __builtin_bit_cast(double, r);
+}
+// Exchanges that join ever larger blocks of equal lanes within a row of 16.
+constexpr int kNeighbour = 0xB1;   // quad_perm 1 0 3 2
+constexpr int kPair = 0x4E;        // quad_perm 2 3 0 1
+constexpr int kQuad = 0x141;       // row_half_mirror
+constexpr int kHalf = 0x140;       // row_mirror
+
+template <typename F>
+__device__ __forceinline__ float row_all(float v, F f) {
+  v = f(v, dpp_f<kNeighbour>(v));
+  v = f(v, dpp_f<kPair>(v));
+  v = f(v, dpp_f<kQuad>(v));
+  return f(v, dpp_f<kHalf>(v));
+}
+__device__ __forceinline__ float add_f(float x, float y) { return x + y; }
+__device__ __forceinline__ float max_f(float x, float y) { return fmaxf(x, y); }
+__device__ __forceinline__ float min_f(float x, float y) { return fminf(x, y); }
+
+__device__ __forceinline__ double row_sum(double v) {
+  v += dpp_d<kNeighbour>(v);
+  v += dpp_d<kPair>(v);
+  v += dpp_d<kQuad>(v);
+  return v + dpp_d<kHalf>(v);
+}
+
+// 32 bits that order like the fp32 (both zeros equal), and back.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __builtin_bit_cast(float, o ^ (~(uint32_t)((int32_t)o >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ double packed(uint32_t order, int index) {
+  const uint32_t hi = 0x3FF00000u | (order >> 12), lo = order << 20 | (uint32_t)(1023 - index);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ int packed_index(double v) {
+  return 1023 - (int)(__builtin_bit_cast(uint64_t, v) & 1023);
+}
+__device__ __forceinline__ uint32_t packed_order(double v) {
+  return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 20);
+}
+
+__device__ __forceinline__ void order_pair(double& x, double& y, bool down) {
+  const double hi = fmax(x, y), lo = fmin(x, y);
+  x = down ? hi : lo;
+  y = down ? lo : hi;
+}
+// A bitonic list into descending order.
+template <int K>
+__device__ __forceinline__ void merge_down(double (&v)[K]) {
+#pragma unroll
+  for (int d = K / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if ((i & d) == 0) order_pair(v[i], v[i + d], true);
+}
+template <int K>
+__device__ __forceinline__ void sort_down(double (&v)[K]) {
+#pragma unroll
+  for (int n = 2; n <= K; n *= 2)
+#pragma unroll
+    for (int d = n / 2; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if ((i & d) == 0) order_pair(v[i], v[i + d], (i & n) == 0 || n == K);
+}
+template <int CTRL, int K>
+__device__ __forceinline__ void join_lists(double (&v)[K]) {
+  double o[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) o[i] = dpp_d<CTRL>(v[K - 1 - i]);
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = fmax(v[i], o[i]);
+  merge_down(v);
+}
+
+template <int V, int K, bool SCORED>
+__global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
+  extern __shared__ double choices[];  // [4][e], for exact_row with groups
+  const int li = threadIdx.x & 15;
+  const int wave = threadIdx.x >> 6;
+  const long tok = (long)blockIdx.x * kRowTokens + (threadIdx.x >> 4);
+  const float* row = a.logits + (tok < a.t ? tok : a.t - 1) * a.e;
+  const int per = (a.e + 15) >> 4;
+  const int e0 = li * per;
+  const float inf = __builtin_inff();
+
+  float l[V];
+  if ((per & 3) == 0 && a.e == per * 16 && ((uintptr_t)a.logits & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = i < per ? *reinterpret_cast<const float4*>(row + e0 + i) : make_float4(-inf, -inf, -inf, -inf);
+      l[i] = f.x;
+      l[i + 1] = f.y;
+      l[i + 2] = f.z;
+      l[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = i < per && e0 + i < a.e ? row[e0 + i] : -inf;
+  }
+  const int own = per < a.e - e0 ? per : a.e - e0;  // experts of this lane (none: <= 0)
+
+  bool slow = false;
+  float c[V];  // choices
+  float top = -inf;
+#pragma unroll
+  for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+  top = row_all(top, max_f);
+  if constexpr (SCORED) {
+    constexpr float log2e = 1.4426950408889634f;
+    if (a.score == 0) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        c[i] = __builtin_amdgcn_exp2f((l[i] - top) * log2e);
+        sum += i < own ? c[i] : 0.0f;
+      }
+      const float r = __builtin_amdgcn_rcpf(row_all(sum, add_f));
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] *= r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -log2e));
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] += i < own ? a.bias[e0 + i] : 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = l[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    slow |= i < own && (c[i] != c[i] || l[i] != l[i] || (!SCORED && a.score == 0 && c[i] == inf));
+
+  bool kept = true;  // this lane's group (the host sends only groups of whole lanes here)
+  if (a.groups > 1) {
+    float first = -inf, second = -inf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float v = i < own ? c[i] : -inf;
+      second = fmaxf(second, fminf(first, v));
+      first = fmaxf(first, v);
+    }
+    const int lanes = 16 / a.groups;
+    auto join = [&](float f, float s) {
+      second = fmaxf(fmaxf(second, s), fminf(first, f));
+      first = fmaxf(first, f);
+    };
+    if (lanes > 1) join(dpp_f<kNeighbour>(first), dpp_f<kNeighbour>(second));
+    if (lanes > 2) join(dpp_f<kPair>(first), dpp_f<kPair>(second));
+    if (lanes > 4) join(dpp_f<kQuad>(first), dpp_f<kQuad>(second));
+    const float g = a.group_top == 1 ? first : first + second;
+    const double mine = packed(ordered(g), li / lanes);
+    int better_lanes = 0;
+#define QMM_TOPK_AGAINST(r) better_lanes += dpp_d<0x120 + r>(mine) > mine;  // row_ror:r
+    QMM_TOPK_AGAINST(1) QMM_TOPK_AGAINST(2) QMM_TOPK_AGAINST(3) QMM_TOPK_AGAINST(4) QMM_TOPK_AGAINST(5)
+    QMM_TOPK_AGAINST(6) QMM_TOPK_AGAINST(7) QMM_TOPK_AGAINST(8) QMM_TOPK_AGAINST(9) QMM_TOPK_AGAINST(10)
+    QMM_TOPK_AGAINST(11) QMM_TOPK_AGAINST(12) QMM_TOPK_AGAINST(13) QMM_TOPK_AGAINST(14) QMM_TOPK_AGAINST(15)
+#undef QMM_TOPK_AGAINST
+    kept = better_lanes < a.group_keep * lanes;
+    if constexpr (SCORED) {
+      const float err = a.group_top == 1 ? 0x1p-20f + 0x1p-22f * fabsf(first)
+                                         : 0x1p-19f + 0x1p-22f * (fabsf(first) + fabsf(second));
+      slow |= g != g || !(row_all(kept ? g - err : inf, min_f) > row_all(kept ? -inf : g + err, max_f));
+    }
+  }
+
+  double best[K];
+#pragma unroll
+  for (int base = 0; base < V; base += K) {
+    double part[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      part[i] = base + i < V && base + i < own && kept ? packed(ordered(c[base + i < V ? base + i : 0]), e0 + base + i) : 0.0;
+    sort_down(part);
+    if (base == 0) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) best[i] = part[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; ++i) best[i] = fmax(best[i], part[K - 1 - i]);
+      merge_down(best);
+    }
+  }
+  join_lists<kNeighbour>(best);
+  join_lists<kPair>(best);
+  join_lists<kQuad>(best);
+  join_lists<kHalf>(best);
+
+  int id = li;
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    if (li == j) id = packed_index(best[j]);
+  if constexpr (SCORED) {
+    float last = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (j >= a.top_k) break;
+      const float v = unordered(packed_order(best[j]));
+      if (j > 0) slow |= !(last - v > 0x1p-19f + 0x1p-21f * fabsf(last));
+      last = v;
+    }
+    const float border = last - (0x1p-19f + 0x1p-21f * fabsf(last));
+    int near = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) near += i < own && kept && !(c[i] < border);
+    slow |= row_all((float)near, add_f) != (float)a.top_k;
+  }
+
+  // the weights: lane j has the j-th chosen expert
+  const bool mine = li < a.top_k;
+  const uint64_t again = __ballot(slow);  // lanes of all four tokens
+  const float v = mine ? row[id < a.e ? id : 0] : -inf;
+  double w;
+  if (a.renormalize) {
+    const float ref = row_all(v, max_f);
+    const double s = !mine ? 0.0 : a.score != 0 ? 1.0 / (1.0 + exp(-(double)v))
+                   : v > -inf ? exp((double)v - (double)ref) : 0.0;
+    const double sum = row_sum(s);
+    w = sum > 0.0 ? s / sum : 0.0;
+  } else if (a.score != 0) {
+    w = 1.0 / (1.0 + exp(-(double)v));
+  } else {
+    double total = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < own && l[i] > -inf) total += exp((double)l[i] - (double)top);
+    total = row_sum(total);
+    w = v > -inf ? exp((double)v - (double)top) / total : 0.0;
+  }
+  const int part = (threadIdx.x >> 4) & 3;
+  if (mine && tok < a.t && !((again >> (part * 16)) & 0xFFFF)) {
+    a.ids[tok * a.top_k + li] = id;
+    a.weights[tok * a.top_k + li] = (float)(w * (double)a.scale);
+  }
+  if (again == 0) return;
+  for (int i = 0; i < 4; ++i) {
+    const long other = (long)blockIdx.x * kRowTokens + wave * 4 + i;
+    if (((again >> (i * 16)) & 0xFFFF) && other < a.t) exact_row<(V + 3) / 4>(a, other, choices + (size_t)wave * a.e);
+  }
+}
+
+template <int V, int K>
+static void launch_row(const TopkArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(((long)a.t + kRowTokens - 1) / kRowTokens)), block(256);
+  const size_t lds = a.groups > 1 ? (size_t)4 * a.e * sizeof(double) : 0;
+  if (a.bias != nullptr || a.group_top == 2) hipLaunchKernelGGL((moe_topk_row_kernel<V, K, true>), grid, block, lds, st, a);
+  else hipLaunchKernelGGL((moe_topk_row_kernel<V, K, false>), grid, block, lds, st, a);
+}
+
+template <int V>
+static void launch_wave(const TopkArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(((long)a.t + kTopkWaves - 1) / kTopkWaves)), block(kTopkWaves * 64);
   const size_t lds = a.groups > 1 ? (size_t)kTopkWaves * a.e * sizeof(double) : 0;
-  const int v = (a.e + 63) / 64;
-  if (v <= 1) hipLaunchKernelGGL(moe_topk_kernel<1>, grid, block, lds, st, a);
-  else if (v <= 2) hipLaunchKernelGGL(moe_topk_kernel<2>, grid, block, lds, st, a);
-  else if (v <= 4) hipLaunchKernelGGL(moe_topk_kernel<4>, grid, block, lds, st, a);
-  else if (v <= 8) hipLaunchKernelGGL(moe_topk_kernel<8>, grid, block, lds, st, a);
-  else hipLaunchKernelGGL(moe_topk_kernel<16>, grid, block, lds, st, a);
+  hipLaunchKernelGGL(moe_topk_wave_kernel<V>, grid, block, lds, st, a);
+}
+
+// Sixteen lanes a token where a lane's experts fit its registers, the list of
+// chosen ones its 16 lanes, and groups are made of whole lanes.
+hipError_t launch_moe_topk(const TopkArgs& a, hipStream_t st) {
+  const bool rows = a.e <= 512 && a.top_k <= 16 && (a.groups == 1 || (a.e % 16 == 0 && 16 % a.groups == 0));
+  if (rows) {
+    const int per = (a.e + 15) / 16;
+    if (a.top_k <= 8) {
+      if (per <= 4) launch_row<4, 8>(a, st);
+      else if (per <= 8) launch_row<8, 8>(a, st);
+      else if (per <= 16) launch_row<16, 8>(a, st);
+      else launch_row<32, 8>(a, st);
+    } else {
+      if (per <= 4) launch_row<4, 16>(a, st);
+      else if (per <= 8) launch_row<8, 16>(a, st);
+      else if (per <= 16) launch_row<16, 16>(a, st);
+      else launch_row<32, 16>(a, st);
+    }
+  } else {
+    const int v = (a.e + 63) / 64;
+    if (v <= 2) launch_wave<2>(a, st);
+    else if (v <= 4) launch_wave<4>(a, st);
+    else if (v <= 8) launch_wave<8>(a, st);
+    else launch_wave<16>(a, st);
+  }
   return hipGetLastError();
 }
 

@@ -591,7 +591,8 @@ int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, fl
                  int renormalize, float scale, qmm_stream stream) {
   const char* fn = "qmm_moe_topk";
   clear_error();
-  if (t < 0) return fail(QMM_ERR_INVALID_ARG, "%s: t=%d must be >= 0", fn, t);
+  if (t < 0 || t > qmm::kTopkTokens)
+    return fail(QMM_ERR_INVALID_ARG, "%s: t=%d must be in [0, %d]", fn, t, qmm::kTopkTokens);
   if (e < 1 || e > kMaxExperts)
     return fail(QMM_ERR_INVALID_ARG, "%s: e=%d must be in [1, %d]", fn, e, kMaxExperts);
   if (score != QMM_SCORE_SOFTMAX && score != QMM_SCORE_SIGMOID)

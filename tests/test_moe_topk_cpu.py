@@ -20,6 +20,7 @@ def call(logits=A, bias=None, ids=A, weights=A, t=4, e=128, top_k=8, score=0, gr
 
 @pytest.mark.parametrize("kw, status, text", [
     (dict(t=-1), INV, "t=-1"),
+    (dict(t=1 << 26), INV, "t=67108864"),
     (dict(e=0), INV, "e=0"),
     (dict(e=1025), INV, "e=1025"),
     (dict(score=2), UNS, "score=2"),
