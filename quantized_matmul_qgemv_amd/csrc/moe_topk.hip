@@ -28,16 +28,49 @@ __device__ __forceinline__ bool better(double ca, int ea, double cb, int eb) {
   return ca > cb || (ca == cb && ea < eb);
 }
 
-__device__ __forceinline__ void wave_best(double& c, int& e) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const double oc = __shfl_xor(c, d, 64);
-    const int oe = __shfl_xor(e, d, 64);
-    if (better(oc, oe, c, e)) {
-      c = oc;
-      e = oe;
-    }
-  }
+// A value of another lane: permutations within the rows of 16 lanes (all
+// lanes read a valid one), and the last lane of one row or two rows before.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(v, v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t r = (uint64_t)dpp<CTRL, ROWS>((uint32_t)(u >> 32)) << 32 | dpp<CTRL, ROWS>((uint32_t)u);
+  return __builtin_bit_cast(double, r);
+}
+// Exchanges that join ever larger blocks of equal lanes within a row of 16,
+// then (the rows that receive are 1 and 3, then 2 and 3) whole rows up to
+// lane 63.
+constexpr int kNeighbour = 0xB1;  // quad_perm 1 0 3 2
+constexpr int kPair = 0x4E;       // quad_perm 2 3 0 1
+constexpr int kQuad = 0x141;      // row_half_mirror
+constexpr int kHalf = 0x140;      // row_mirror
+constexpr int kRow = 0x142;       // row_bcast:15
+constexpr int kTwoRows = 0x143;   // row_bcast:31
+
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ void join_best(double& c, int& e) {
+  const double oc = dpp_d<CTRL, ROWS>(c);
+  const int oe = (int)dpp<CTRL, ROWS>((uint32_t)e);
+  const bool take = better(oc, oe, c, e);
+  c = take ? oc : c;
+  e = take ? oe : e;
+}
+// The index of the wave's best choice (-1 if there is none), in all lanes.
+__device__ __forceinline__ int wave_best(double c, int e) {
+  join_best<kNeighbour>(c, e);
+  join_best<kPair>(c, e);
+  join_best<kQuad>(c, e);
+  join_best<kHalf>(c, e);
+  join_best<kRow, 0xA>(c, e);
+  join_best<kTwoRows, 0xC>(c, e);
+  return __builtin_amdgcn_readlane(e, 63);
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -106,14 +139,12 @@ __device__ void exact_row(const TopkArgs& a, long tok, double* choices) {
     double g = 0.0;
     if (lane < a.groups) {
       double first = -__builtin_inf(), second = -__builtin_inf();
+#pragma unroll 4
       for (int j = 0; j < size; ++j) {
         const double v = choices[lane * size + j];
-        if (v > first) {
-          second = first;
-          first = v;
-        } else if (v > second) {
-          second = v;
-        }
+        second = fmax(second, fmin(first, v));
+        first = fmax(first, v);
+        bad |= v != v;
       }
       g = a.group_top == 1 ? first : first + second;
       bad |= g != g;
@@ -122,9 +153,7 @@ __device__ void exact_row(const TopkArgs& a, long tok, double* choices) {
     int own = lane < a.groups ? lane : -1;
     uint64_t keep = 0;
     for (int j = 0; j < a.group_keep; ++j) {
-      double gb = g;
-      int gi = own;
-      wave_best(gb, gi);
+      const int gi = wave_best(g, own);
       if (gi < 0) break;  // only where a row holds a NaN
       keep |= 1ull << gi;
       if (own == gi) own = -1;
@@ -150,7 +179,7 @@ __device__ void exact_row(const TopkArgs& a, long tok, double* choices) {
         eb = e;
       }
     }
-    wave_best(cb, eb);
+    eb = wave_best(cb, eb);
     if (lane == j) id = eb;
     if ((eb & 63) == lane) alive &= ~(1u << (eb >> 6));
   }
@@ -186,42 +215,24 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_wave_kernel(TopkArgs
 // One token by 16 lanes, four tokens a wave; lane i holds the `per` experts
 // from i * per on.
 //
-// A choice is packed with its expert into one 64-bit number that orders like
-// the choice and, where choices are equal, by the lower expert: a double in
-// [1, 2) whose mantissa holds 32 bits that order like the fp32 choice and 10
-// bits of 1023 - expert.  Comparing, then, is v_max_f64 / v_min_f64.  Each
-// lane sorts its experts down to a list of K (K >= top_k) with bitonic
-// networks, and four exchanges along the DPP row (neighbours, pairs, quads,
-// halves) merge the lists: max(a[i], b[K-1-i]) are the K largest of two
-// sorted lists, one more bitonic pass sorts them.
-//
-// Where the scores themselves are compared (SCORED) this runs on fp32 scores,
-// whose error is at most 2^-21 + 2^-23 |c| (exp2 and rcp to one unit, the
-// rounded argument: |l| s (1 - s) < 0.28), and is right unless two choices
-// that matter are nearer than twice that: neighbours among the chosen, the
-// last chosen and any other, a kept group and a dropped one.  Such rows, and
-// rows with a NaN, an infinite sum or nothing but -inf, go to exact_row.
+// A choice and its expert are packed into one double that orders like the
+// choice, so that comparing is v_max_f64 / v_min_f64.  Each lane sorts its
+// experts down to a list of K (K >= top_k) with bitonic networks, and four
+// exchanges along the DPP row (neighbours, pairs, quads, halves) merge the
+// lists: max(a[i], b[K-1-i]) are the K largest of two sorted lists, one more
+// bitonic pass sorts them.
+//   By logit: a double in [1, 2) whose mantissa holds 32 bits that order like
+//     the logit and below them 1023 - expert: equal logits order by the
+//     lower expert.
+//   SCORED: the fp32 choice as a double, its place (lane, element) in the 29
+//     bits that are free.  The fp32 choice is off by at most
+//     2^-21 + 2^-23 |c| (exp2 and rcp to one unit; the rounded argument's
+//     part: |l| s (1 - s) < 0.28).  Where two that matter are nearer than
+//     twice that, they are formed again in 64 bits: the groups' scores before
+//     any is dropped, and after the merge all experts that are no further
+//     than that below the last chosen one, one for each lane.
+// Rows with a NaN, an infinity or more than 16 such experts go to exact_row.
 constexpr int kRowTokens = 16;  // tokens per workgroup of 256
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp_f(float v) {
-  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp_d(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint64_t r = (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u);
-  return __builtin_bit_cast(double, r);
-}
-// Exchanges that join ever larger blocks of equal lanes within a row of 16.
-constexpr int kNeighbour = 0xB1;   // quad_perm 1 0 3 2
-constexpr int kPair = 0x4E;        // quad_perm 2 3 0 1
-constexpr int kQuad = 0x141;       // row_half_mirror
-constexpr int kHalf = 0x140;       // row_mirror
 
 template <typename F>
 __device__ __forceinline__ float row_all(float v, F f) {
@@ -240,25 +251,34 @@ __device__ __forceinline__ double row_sum(double v) {
   v += dpp_d<kQuad>(v);
   return v + dpp_d<kHalf>(v);
 }
+__device__ __forceinline__ double row_max(double v) {
+  v = fmax(v, dpp_d<kNeighbour>(v));
+  v = fmax(v, dpp_d<kPair>(v));
+  v = fmax(v, dpp_d<kQuad>(v));
+  return fmax(v, dpp_d<kHalf>(v));
+}
 
-// 32 bits that order like the fp32 (both zeros equal), and back.
-__device__ __forceinline__ uint32_t ordered(float f) {
+// How many of the other 15 lanes of the row hold a value that comes before
+// (v, tie): a larger v, or an equal one with a lower tie.
+template <int R = 1>
+__device__ __forceinline__ int lanes_before(double v, int tie) {
+  if constexpr (R == 16) {
+    return 0;
+  } else {
+    const double o = dpp_d<0x120 + R>(v);  // row_ror:R
+    const int t = (int)dpp<0x120 + R>((uint32_t)tie);
+    return (o > v || (o == v && t < tie)) + lanes_before<R + 1>(v, tie);
+  }
+}
+
+// 32 bits that order like the fp32 (both zeros equal), above 1023 - index.
+__device__ __forceinline__ double packed(float f, int index) {
   const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);
-  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t o) {
-  return __builtin_bit_cast(float, o ^ (~(uint32_t)((int32_t)o >> 31) | 0x80000000u));
-}
-__device__ __forceinline__ double packed(uint32_t order, int index) {
+  const uint32_t order = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
   const uint32_t hi = 0x3FF00000u | (order >> 12), lo = order << 20 | (uint32_t)(1023 - index);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ int packed_index(double v) {
-  return 1023 - (int)(__builtin_bit_cast(uint64_t, v) & 1023);
-}
-__device__ __forceinline__ uint32_t packed_order(double v) {
-  return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 20);
-}
+__device__ __forceinline__ uint32_t low_bits(double v) { return (uint32_t)__builtin_bit_cast(uint64_t, v); }
 
 __device__ __forceinline__ void order_pair(double& x, double& y, bool down) {
   const double hi = fmax(x, y), lo = fmin(x, y);
@@ -295,7 +315,7 @@ __device__ __forceinline__ void join_lists(double (&v)[K]) {
 }
 
 template <int V, int K, bool SCORED>
-__global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V > 16 ? 2 : 4))) void moe_topk_row_kernel(TopkArgs a) {
   extern __shared__ double choices[];  // [4][e], for exact_row with groups
   const int li = threadIdx.x & 15;
   const int wave = threadIdx.x >> 6;
@@ -303,7 +323,9 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
   const float* row = a.logits + (tok < a.t ? tok : a.t - 1) * a.e;
   const int per = (a.e + 15) >> 4;
   const int e0 = li * per;
+  const int own = per < a.e - e0 ? per : a.e - e0;  // experts of this lane (none: <= 0)
   const float inf = __builtin_inff();
+  constexpr float kOut = -3.402823466e38f;  // SCORED: no choice (real ones stay within 1e38)
 
   float l[V];
   if ((per & 3) == 0 && a.e == per * 16 && ((uintptr_t)a.logits & 15) == 0) {
@@ -317,24 +339,26 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = i < per && e0 + i < a.e ? row[e0 + i] : -inf;
+    for (int i = 0; i < V; ++i) l[i] = i < own ? row[e0 + i] : -inf;
   }
-  const int own = per < a.e - e0 ? per : a.e - e0;  // experts of this lane (none: <= 0)
 
   bool slow = false;
   float c[V];  // choices
   float top = -inf;
+  if (a.score == 0) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
-  top = row_all(top, max_f);
+    for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+    top = row_all(top, max_f);
+  }
+  float finite = 0.0f;  // NaN if anything is not
   if constexpr (SCORED) {
     constexpr float log2e = 1.4426950408889634f;
     if (a.score == 0) {
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        c[i] = __builtin_amdgcn_exp2f((l[i] - top) * log2e);
-        sum += i < own ? c[i] : 0.0f;
+        c[i] = __builtin_amdgcn_exp2f((l[i] - top) * log2e);  // 0 beyond the lane's own
+        sum += c[i];
       }
       const float r = __builtin_amdgcn_rcpf(row_all(sum, add_f));
 #pragma unroll
@@ -347,16 +371,40 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] += i < own ? a.bias[e0 + i] : 0.0f;
     }
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      finite = fmaf(c[i], 0.0f, finite);
+      big = fmaxf(big, fabsf(c[i]));
+    }
+    slow = !(big < 1e38f);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = l[i];
-  }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    slow |= i < own && (c[i] != c[i] || l[i] != l[i] || (!SCORED && a.score == 0 && c[i] == inf));
+    for (int i = 0; i < V; i += 2) slow |= __builtin_isunordered(l[i], l[i + 1]);
+    slow |= a.score == 0 && top == inf;
+  }
+  slow |= finite != finite;
+
+  // The choice in 64 bits, of logit v and bias index e; the softmax's sum.
+  double total = 0.0;
+  auto exact_total = [&]() {
+    total = 0.0;
+    if (a.score == 0) {
+#pragma unroll 2
+      for (int i = 0; i < own; ++i) total += exp((double)row[e0 + i] - (double)top);
+      total = row_sum(total);
+    }
+  };
+  auto exact_choice = [&](float v, int e) -> double {
+    const double s = a.score != 0 ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top) / total;
+    return a.bias != nullptr ? s + (double)a.bias[e] : s;
+  };
 
   bool kept = true;  // this lane's group (the host sends only groups of whole lanes here)
   if (a.groups > 1) {
+    const int lanes = 16 / a.groups;
     float first = -inf, second = -inf;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -364,7 +412,6 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
       second = fmaxf(second, fminf(first, v));
       first = fmaxf(first, v);
     }
-    const int lanes = 16 / a.groups;
     auto join = [&](float f, float s) {
       second = fmaxf(fmaxf(second, s), fminf(first, f));
       first = fmaxf(first, f);
@@ -372,29 +419,50 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
     if (lanes > 1) join(dpp_f<kNeighbour>(first), dpp_f<kNeighbour>(second));
     if (lanes > 2) join(dpp_f<kPair>(first), dpp_f<kPair>(second));
     if (lanes > 4) join(dpp_f<kQuad>(first), dpp_f<kQuad>(second));
-    const float g = a.group_top == 1 ? first : first + second;
-    const double mine = packed(ordered(g), li / lanes);
-    int better_lanes = 0;
-#define QMM_TOPK_AGAINST(r) better_lanes += dpp_d<0x120 + r>(mine) > mine;  // row_ror:r
-    QMM_TOPK_AGAINST(1) QMM_TOPK_AGAINST(2) QMM_TOPK_AGAINST(3) QMM_TOPK_AGAINST(4) QMM_TOPK_AGAINST(5)
-    QMM_TOPK_AGAINST(6) QMM_TOPK_AGAINST(7) QMM_TOPK_AGAINST(8) QMM_TOPK_AGAINST(9) QMM_TOPK_AGAINST(10)
-    QMM_TOPK_AGAINST(11) QMM_TOPK_AGAINST(12) QMM_TOPK_AGAINST(13) QMM_TOPK_AGAINST(14) QMM_TOPK_AGAINST(15)
-#undef QMM_TOPK_AGAINST
-    kept = better_lanes < a.group_keep * lanes;
+    const float g = (a.group_top == 1 ? first : first + second) + 0.0f;
+    const int most = a.group_keep * lanes;
+    kept = lanes_before((double)g, li / lanes) < most;
     if constexpr (SCORED) {
       const float err = a.group_top == 1 ? 0x1p-20f + 0x1p-22f * fabsf(first)
                                          : 0x1p-19f + 0x1p-22f * (fabsf(first) + fabsf(second));
-      slow |= g != g || !(row_all(kept ? g - err : inf, min_f) > row_all(kept ? -inf : g + err, max_f));
+      const bool near = !(row_all(kept ? g - err : inf, min_f) > row_all(kept ? -inf : g + err, max_f));
+      if (__any(near && !slow)) {
+        exact_total();
+        double f1 = -__builtin_inf(), f2 = f1;
+#pragma unroll 1
+        for (int i = 0; i < own; ++i) {
+          const double v = exact_choice(row[e0 + i], e0 + i);
+          f2 = fmax(f2, fmin(f1, v));
+          f1 = fmax(f1, v);
+        }
+        auto join64 = [&](double f, double s) {
+          f2 = fmax(fmax(f2, s), fmin(f1, f));
+          f1 = fmax(f1, f);
+        };
+        if (lanes > 1) join64(dpp_d<kNeighbour>(f1), dpp_d<kNeighbour>(f2));
+        if (lanes > 2) join64(dpp_d<kPair>(f1), dpp_d<kPair>(f2));
+        if (lanes > 4) join64(dpp_d<kQuad>(f1), dpp_d<kQuad>(f2));
+        kept = lanes_before(a.group_top == 1 ? f1 : f1 + f2, li / lanes) < most;
+      }
     }
   }
 
+  const int mine_n = kept ? own : 0;  // of this lane's experts, those that may be chosen
   double best[K];
 #pragma unroll
   for (int base = 0; base < V; base += K) {
     double part[K];
 #pragma unroll
-    for (int i = 0; i < K; ++i)
-      part[i] = base + i < V && base + i < own && kept ? packed(ordered(c[base + i < V ? base + i : 0]), e0 + base + i) : 0.0;
+    for (int i = 0; i < K; ++i) {
+      const int at = base + i < V ? base + i : 0;
+      if constexpr (SCORED) {
+        if (base + i < V) c[at] = base + i < mine_n ? c[at] : kOut;
+        const double d = base + i < V ? (double)c[at] : (double)kOut;
+        part[i] = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, d) | (uint64_t)(li << 5 | at));
+      } else {
+        part[i] = base + i < V && base + i < mine_n ? packed(c[at], e0 + at) : 0.0;
+      }
+    }
     sort_down(part);
     if (base == 0) {
 #pragma unroll
@@ -410,24 +478,50 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
   join_lists<kQuad>(best);
   join_lists<kHalf>(best);
 
-  int id = li;
+  // lane j takes the j-th of the list
+  double got = best[0];
 #pragma unroll
-  for (int j = 0; j < K; ++j)
-    if (li == j) id = packed_index(best[j]);
+  for (int j = 1; j < K; ++j) got = li == j ? best[j] : got;
+  auto expert_of = [&](double v) {
+    const int low = (int)low_bits(v);
+    return SCORED ? ((low >> 5) & 15) * per + (low & 31) : 1023 - (low & 1023);
+  };
+  int id = expert_of(got);
   if constexpr (SCORED) {
-    float last = 0.0f;
+    const float v = (float)got;
+    const float err = 0x1p-19f + 0x1p-21f * fabsf(v);
+    // the lane before holds the next larger one (row_shr:1)
+    const float before = dpp_f<0x111>(v);
+    bool near = li > 0 && li < a.top_k && !(before - v > err);
+    const float border = row_all(li < a.top_k ? v - err : inf, min_f);
+    int n = 0;
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      if (j >= a.top_k) break;
-      const float v = unordered(packed_order(best[j]));
-      if (j > 0) slow |= !(last - v > 0x1p-19f + 0x1p-21f * fabsf(last));
-      last = v;
+    for (int i = 0; i < V; ++i) n += c[i] >= border;
+    const int count = (int)row_all((float)n, add_f);
+    near |= count != a.top_k;
+    slow |= count > 16;
+    if (__any(near && !slow)) {
+      exact_total();
+      // experts beyond the list that are near, one after the other
+      double below = best[K - 1];
+#pragma unroll 1
+      for (int j = K; j < 16 && __any(j < count && !slow); ++j) {
+        double next = -__builtin_inf();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const double d = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, (double)c[i]) | (uint64_t)(li << 5 | i));
+          if (d < below) next = fmax(next, d);
+        }
+        below = row_max(next);
+        if (li == j) id = expert_of(below);
+      }
+      const bool in = li < count;
+      const bool ok = in && id < a.e;
+      const double e64 = ok ? exact_choice(row[id], id) : -__builtin_inf();
+      // lanes without an expert keep their place behind the others
+      const int to = (threadIdx.x & 48) + (in ? lanes_before(e64, ok ? id : 1024 + li) : li);
+      id = __builtin_amdgcn_ds_permute(to << 2, id);
     }
-    const float border = last - (0x1p-19f + 0x1p-21f * fabsf(last));
-    int near = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) near += i < own && kept && !(c[i] < border);
-    slow |= row_all((float)near, add_f) != (float)a.top_k;
   }
 
   // the weights: lane j has the j-th chosen expert
@@ -444,11 +538,7 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
   } else if (a.score != 0) {
     w = 1.0 / (1.0 + exp(-(double)v));
   } else {
-    double total = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < own && l[i] > -inf) total += exp((double)l[i] - (double)top);
-    total = row_sum(total);
+    exact_total();
     w = v > -inf ? exp((double)v - (double)top) / total : 0.0;
   }
   const int part = (threadIdx.x >> 4) & 3;
