@@ -271,6 +271,18 @@ __device__ __forceinline__ int lanes_before(double v, int tie) {
   }
 }
 
+// How many groups of `lanes` lanes hold a larger value.
+template <int R = 1>
+__device__ __forceinline__ int groups_before(float v, int lanes) {
+  if constexpr (R == 16) {
+    return 0;
+  } else {
+    int n = groups_before<R + 1>(v, lanes);
+    if ((R & (lanes - 1)) == 0) n += dpp_f<0x120 + R>(v) > v;  // row_ror:R
+    return n;
+  }
+}
+
 // 32 bits that order like the fp32 (both zeros equal), above 1023 - index.
 __device__ __forceinline__ double packed(float f, int index) {
   const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);
@@ -314,6 +326,29 @@ __device__ __forceinline__ void join_lists(double (&v)[K]) {
   merge_down(v);
 }
 
+// A lane's own values of one row: by 16 bytes where every lane has `per` of
+// them and the rows are aligned; `rest` beyond them.
+template <int V>
+__device__ __forceinline__ void load_own(float (&v)[V], const float* p, int e0, int own, int e, int per, bool wide,
+                                         float rest) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      float4 f = make_float4(rest, rest, rest, rest);
+      if (i < per) f = *reinterpret_cast<const float4*>(p + e0 + i);
+      v[i] = f.x;
+      v[i + 1] = f.y;
+      v[i + 2] = f.z;
+      v[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p[e0 + i < e ? e0 + i : e - 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < own ? v[i] : rest;
+  }
+}
+
 template <int V, int K, bool SCORED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V > 16 ? 2 : 4))) void moe_topk_row_kernel(TopkArgs a) {
   extern __shared__ double choices[];  // [4][e], for exact_row with groups
@@ -328,19 +363,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V > 16 ? 2 
   constexpr float kOut = -3.402823466e38f;  // SCORED: no choice (real ones stay within 1e38)
 
   float l[V];
-  if ((per & 3) == 0 && a.e == per * 16 && ((uintptr_t)a.logits & 15) == 0) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 f = i < per ? *reinterpret_cast<const float4*>(row + e0 + i) : make_float4(-inf, -inf, -inf, -inf);
-      l[i] = f.x;
-      l[i + 1] = f.y;
-      l[i + 2] = f.z;
-      l[i + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = i < own ? row[e0 + i] : -inf;
-  }
+  const bool whole = (per & 3) == 0 && a.e == per * 16;
+  load_own<V>(l, row, e0, own, a.e, per, whole && ((uintptr_t)a.logits & 15) == 0, -inf);
 
   bool slow = false;
   float c[V];  // choices
@@ -368,8 +392,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V > 16 ? 2 
       for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -log2e));
     }
     if (a.bias != nullptr) {
+      float b[V];
+      load_own<V>(b, a.bias, e0, own, a.e, per, whole && ((uintptr_t)a.bias & 15) == 0, 0.0f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] += i < own ? a.bias[e0 + i] : 0.0f;
+      for (int i = 0; i < V; ++i) c[i] += b[i];
     }
     float big = 0.0f;
 #pragma unroll
@@ -421,11 +447,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V > 16 ? 2 
     if (lanes > 4) join(dpp_f<kQuad>(first), dpp_f<kQuad>(second));
     const float g = (a.group_top == 1 ? first : first + second) + 0.0f;
     const int most = a.group_keep * lanes;
-    kept = lanes_before((double)g, li / lanes) < most;
-    if constexpr (SCORED) {
+    if constexpr (!SCORED) {
+      kept = lanes_before((double)g, li / lanes) < most;
+    } else {
+      kept = groups_before(g, lanes) * lanes < most;  // nearly equal ones are told apart below
       const float err = a.group_top == 1 ? 0x1p-20f + 0x1p-22f * fabsf(first)
                                          : 0x1p-19f + 0x1p-22f * (fabsf(first) + fabsf(second));
-      const bool near = !(row_all(kept ? g - err : inf, min_f) > row_all(kept ? -inf : g + err, max_f));
+      const uint32_t keeping = (uint32_t)(__ballot(kept) >> (threadIdx.x & 48)) & 0xFFFF;  // too many where some are equal
+      const bool near = __popc(keeping) != most ||
+                        !(row_all(kept ? g - err : inf, min_f) > row_all(kept ? -inf : g + err, max_f));
       if (__any(near && !slow)) {
         exact_total();
         double f1 = -__builtin_inf(), f2 = f1;

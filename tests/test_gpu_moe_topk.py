@@ -181,6 +181,38 @@ def test_choice_between_neighbours(score, groups, top):
     compare(l2, 8, b, score="sigmoid", groups=groups, group_keep=max(1, groups // 2), group_top=top)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e, top_k, groups, top", [(64, 8, 1, 1), (64, 5, 1, 1), (128, 16, 1, 1), (256, 8, 8, 2), (48, 3, 4, 1),
+                                                   (500, 6, 1, 1)])
+def test_some_neighbours(score, e, top_k, groups, top):
+    """A handful of experts, fewer and more than are chosen, nearer to each
+    other than fp32 scores tell apart, the others far; and groups of them."""
+    say("moe_topk some neighbours", score, e, top_k, groups, top)
+    r = np.random.default_rng([79, e, top_k])
+    rows, biases = [], (r.standard_normal(e) * 0.01).astype(np.float32)
+    for n in list(range(1, 19)) * 4:
+        l = np.clip(r.standard_normal(e), -2, 2) - 4.0
+        at = r.permutation(e)[:n]
+        high = r.permutation(e)[:max(0, top_k - 1 - n // 2)]
+        l[high] = 3 + r.random(len(high))
+        l = l.astype(np.float32)
+        # in the sum with the bias they meet at one value, apart by a few steps of fp32
+        s = 0.4 - biases[at].astype(np.float64) + r.integers(-3, 4, n) * 2.0 ** -26
+        l[at] = np.log(s / (1 - s)).astype(np.float32) if score == "sigmoid" else np.float32(2.0) + r.integers(-2, 3, n).astype(np.float32) * np.float32(2.0 ** -22)
+        rows.append(l)
+    bias = biases if score == "sigmoid" else np.zeros(e, np.float32)
+    compare(np.stack(rows), top_k, bias, score=score, groups=groups, group_keep=max(1, groups // 2), group_top=top)
+    if groups > 1:  # groups alike but for a step or two of one expert
+        part = r.standard_normal(e // groups).astype(np.float32)
+        l = np.tile(part, (64, groups)).reshape(64, groups, -1)
+        best = int(part.argmax())
+        for i in range(64):
+            for g in range(groups):
+                l[i, g, best] += np.float32(r.integers(-2, 3)) * np.spacing(l[i, g, best])
+        compare(l.reshape(64, e), min(top_k, e // groups), np.zeros(e, np.float32), score=score, groups=groups,
+                group_keep=max(1, groups // 2), group_top=top)
+
+
 def test_other_stream_and_repeat():
     say("moe_topk stream")
     r = np.random.default_rng(76)
