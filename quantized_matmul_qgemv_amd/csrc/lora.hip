@@ -47,6 +47,11 @@ __device__ __forceinline__ int lora_slot(const LoraArgs& g, int p) {
   return e < 0 || e >= g.experts ? kBad : a * g.experts + e;
 }
 
+// The row of x that row p reads.
+__device__ __forceinline__ int lora_x_row(const LoraArgs& g, const LoraProblem& p, int row) {
+  return p.x_row_per_pair || g.top_k == 1 ? row : row / g.top_k;
+}
+
 // A workgroup's rows of one slot.
 template <int BM>
 struct TileRows {
@@ -100,17 +105,17 @@ __device__ __forceinline__ bool read_tile(const LoraArgs& g, int i, TileRows<BM>
 }
 
 // ------------------------------------------------------------------ shrink
-// One workgroup: a tile's rows, up to 64 ranks (RT blocks of 16) and one k
-// range.  Direct: 16 rows, the four waves take turns at 64 values of k and
-// are joined in LDS.  Routed: 64 rows, 16 for each wave.
-// A lane's two 16-byte loads per step are neighbours in k (the same
-// permutation of k for both operands leaves the sum as it is), so a wave's
-// loads cover whole 128-byte lines.
+// Tiles of 16 rows (few rows a slot: the weights are what is read).  One
+// workgroup: up to 64 ranks (RT blocks of 16) and one k range; the four waves
+// take turns at 64 values of k and are joined in LDS.  A lane's two 16-byte
+// loads per step are neighbours in k (the same permutation of k for both
+// operands leaves the sum as it is), so a wave's loads cover whole 128-byte
+// lines.
 template <bool ROUTED, int RT>
-__global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs g) {
-  constexpr int BM = ROUTED ? kLoraTileRows : 16;
-  __shared__ TileRows<BM> tile;
+__global__ __launch_bounds__(kLoraThreads) void lora_shrink16_kernel(LoraArgs g) {
+  __shared__ TileRows<16> tile;
   __shared__ uint64_t masks[kLoraDirectRows / 64];
+  __shared__ f4 part[3][RT][64];
   const LoraProblem& p = g.p[blockIdx.z];
   const int chunks = (p.rank + 63) >> 6;
   const int split = blockIdx.y / chunks;
@@ -122,15 +127,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs g) {
   const int wave = threadIdx.x >> 6;
   const int li = lane & 15;
   const int q = lane >> 4;
-  const int first = ROUTED ? wave * 16 : 0;
-  if (first >= tile.count) return;  // routed only: no barrier follows
 
-  const int slot_row = first + li < tile.count ? first + li : tile.count - 1;
-  const int row = tile.rows[slot_row];
-  const int xrow = p.x_row_per_pair || g.top_k == 1 ? row : row / g.top_k;
-  const int kbeg = split * p.k_per_split;
-  const int kend = kbeg + p.k_per_split < p.k ? kbeg + p.k_per_split : p.k;
-  auto xp = to_global(p.x) + (size_t)xrow * p.k + q * 16;
+  const int row = tile.rows[li < tile.count ? li : tile.count - 1];
+  auto xp = to_global(p.x) + (size_t)lora_x_row(g, p, row) * p.k + q * 16;
   gptr<uint16_t> ap[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
@@ -140,9 +139,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs g) {
   f4 acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-  constexpr int STEP = ROUTED ? 64 : 256;
+  const int kend = (split + 1) * p.k_per_split < p.k ? (split + 1) * p.k_per_split : p.k;
 #pragma unroll 2
-  for (int k = kbeg + (ROUTED ? 0 : wave * 64); k < kend; k += STEP) {
+  for (int k = split * p.k_per_split + wave * 64; k < kend; k += 256) {
     const h8 x0 = *(gptr<h8>)(xp + k), x1 = *(gptr<h8>)(xp + k + 8);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -151,135 +150,247 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs g) {
       acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, x1, acc[i], 0, 0, 0);
     }
   }
-  if constexpr (!ROUTED) {
-    __shared__ f4 part[3][RT][64];
-    if (wave > 0) {
+  if (wave > 0) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) part[wave - 1][i][lane] = acc[i];
-    }
-    __syncthreads();
-    if (wave > 0) return;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) acc[i] += part[0][i][lane] + part[1][i][lane] + part[2][i][lane];
+    for (int i = 0; i < RT; ++i) part[wave - 1][i][lane] = acc[i];
   }
-  if (first + li >= tile.count) return;
+  __syncthreads();
+  if (wave > 0 || li >= tile.count) return;
   float* v = g.v + p.v_offset + ((size_t)split * g.rows + row) * p.rank_pad + r0 + q * 4;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    if (r0 + i * 16 < p.rank) *reinterpret_cast<f4*>(v + i * 16) = acc[i] + part[0][i][lane] + part[1][i][lane] + part[2][i][lane];
+}
+
+// Tiles of 64 rows (many rows a slot: x is what is read).  One workgroup: up
+// to 64 ranks and one k range, in steps of 64 values of k that all threads
+// bring into LDS by whole 128-byte lines (straight into the operand layout,
+// whose neighbouring lanes are 16 different rows, every quad of lanes
+// would touch four lines); each wave multiplies 16 of the rows.  The next
+// step's loads are in flight while one is multiplied.
+constexpr int kStage = 72;  // halves from row to row in LDS: 16 lanes' 16 bytes fall into 64 different banks
+template <int RT>
+__global__ __launch_bounds__(kLoraThreads) void lora_shrink64_kernel(LoraArgs g) {
+  __shared__ TileRows<64> tile;
+  __shared__ __attribute__((aligned(16))) uint16_t xs[2][64 * kStage];
+  __shared__ __attribute__((aligned(16))) uint16_t as[2][RT * 16 * kStage];
+  const LoraProblem& p = g.p[blockIdx.z];
+  const int chunks = (p.rank + 63) >> 6;
+  const int split = blockIdx.y / chunks;
+  const int r0 = (blockIdx.y - split * chunks) * 64;
+  if (split >= p.splits) return;
+  if (!read_tile(g, blockIdx.x, tile)) return;
+  if (tile.slot < 0) return;
+  const int count = tile.count;
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int li = lane & 15;
+  const int q = lane >> 4;
+
+  // staging: 8 threads bring 128 bytes of a row
+  constexpr int XL = 2, AL = (RT + 1) / 2;
+  const int sr = threadIdx.x >> 3;
+  const int sc = (threadIdx.x & 7) * 8;
+  gptr<uint16_t> xp[XL], ap[AL];
+#pragma unroll
+  for (int j = 0; j < XL; ++j) {
+    const int at = sr + 32 * j < count ? sr + 32 * j : count - 1;
+    xp[j] = to_global(p.x) + (size_t)lora_x_row(g, p, tile.rows[at]) * p.k + sc;
+  }
+#pragma unroll
+  for (int j = 0; j < AL; ++j) {
+    const int r = r0 + sr + 32 * j < p.rank ? r0 + sr + 32 * j : p.rank - 1;
+    ap[j] = to_global(p.a) + ((size_t)tile.slot * p.rank + r) * p.k + sc;
+  }
+  u32x4 xr[XL], ar[AL];
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < XL; ++j) xr[j] = *(gptr<u32x4>)(xp[j] + k);
+#pragma unroll
+    for (int j = 0; j < AL; ++j) ar[j] = *(gptr<u32x4>)(ap[j] + k);
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int j = 0; j < XL; ++j) *reinterpret_cast<u32x4*>(&xs[buf][(sr + 32 * j) * kStage + sc]) = xr[j];
+#pragma unroll
+    for (int j = 0; j < AL; ++j)
+      if (RT > 1 || sr < 16) *reinterpret_cast<u32x4*>(&as[buf][(sr + 32 * j) * kStage + sc]) = ar[j];
+  };
+  f4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
+  const int kbeg = split * p.k_per_split;
+  const int kend = kbeg + p.k_per_split < p.k ? kbeg + p.k_per_split : p.k;
+  fetch(kbeg);
+  stage(0);
+  int buf = 0;
+  for (int k = kbeg; k < kend; k += 64, buf ^= 1) {
+    __syncthreads();
+    const bool more = k + 64 < kend;
+    if (more) fetch(k + 64);
+    if (wave * 16 < count) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const h8 x = *reinterpret_cast<const h8*>(&xs[buf][(wave * 16 + li) * kStage + h * 32 + q * 8]);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const h8 a = *reinterpret_cast<const h8*>(&as[buf][(i * 16 + li) * kStage + h * 32 + q * 8]);
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x, acc[i], 0, 0, 0);
+        }
+      }
+    }
+    if (more) stage(buf ^ 1);
+  }
+  const int at = wave * 16 + li;
+  if (at >= count) return;
+  float* v = g.v + p.v_offset + ((size_t)split * g.rows + tile.rows[at]) * p.rank_pad + r0 + q * 4;
 #pragma unroll
   for (int i = 0; i < RT; ++i)
     if (r0 + i * 16 < p.rank) *reinterpret_cast<f4*>(v + i * 16) = acc[i];
 }
 
 // ------------------------------------------------------------------ expand
-// One workgroup: a tile's rows and 64 * NT columns, 16 * NT for each wave.
-// KC: 32-wide steps of the contraction over [hi | lo] (2 * rank).  CT: blocks
-// of 16 rows that share a load of B.
-template <bool ROUTED, int KC, int CT, int NT>
+// One workgroup: a tile's BM rows and a range of columns, 64 for each wave at
+// a time.  First all threads sum the rows' partials and leave [hi | lo] in
+// LDS (ranks padded with zeros to 32 * RC).  Then rows x columns on the
+// matrix cores, D[row][column]: block t of a wave's four takes the columns
+// 4 j + t, j = 0 .. 15, so that a lane ends with four neighbouring columns of
+// a row and 16 lanes load base and store y by 256 bytes.
+template <bool ROUTED, int BM, int RC>
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
-  constexpr int BM = ROUTED ? kLoraTileRows : 16;
+  constexpr int CT = BM / 16;
+  constexpr int LD = 2 * RC * 32 + 8;  // halves from row to row in LDS
   __shared__ TileRows<BM> tile;
   __shared__ uint64_t masks[kLoraDirectRows / 64];
+  __shared__ __attribute__((aligned(16))) half_t vs[BM * LD];
+  __shared__ float back[BM];  // what undoes a row's power of two
   const LoraProblem& p = g.p[blockIdx.z];
-  const int n0 = blockIdx.y * (64 * NT);
-  if (n0 >= p.n) return;
+  const int first = blockIdx.y * g.columns;
+  if (first >= p.n) return;
   if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile(g, blockIdx.x, tile, masks))) return;
   const int slot = tile.slot;
+  const int count = tile.count;
+  const int end = first + g.columns < p.n ? first + g.columns : p.n;
+  const bool wide = (p.n & 3) == 0 && ((uintptr_t)p.y & 15) == 0 && ((uintptr_t)p.base & 15) == 0;
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
   if (slot < 0) {
     if (slot == kNone && p.base == p.y) return;
-    const int cols = p.n - n0 < 64 * NT ? p.n - n0 : 64 * NT;
-    for (int i = threadIdx.x; i < tile.count * cols; i += kLoraThreads) {
-      const size_t at = (size_t)tile.rows[i / cols] * p.n + n0 + i % cols;
-      p.y[at] = slot == kBad ? __builtin_nanf("") : p.base ? p.base[at] : 0.0f;
+    for (int i = wave; i < count; i += kLoraThreads / 64) {
+      const size_t at = (size_t)tile.rows[i] * p.n;
+      const float fill = slot == kBad ? __builtin_nanf("") : 0.0f;
+      const float* from = slot == kBad ? nullptr : p.base;
+      if (wide) {
+        for (int n = first + lane * 4; n < end; n += 256)
+          *reinterpret_cast<f4*>(p.y + at + n) = from ? *(gptr<f4>)(to_global(from) + at + n) : f4{fill, fill, fill, fill};
+      } else {
+        for (int n = first + lane; n < end; n += 64) p.y[at + n] = from ? from[at + n] : fill;
+      }
     }
     return;
   }
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int li = lane & 15;
-  const int q = lane >> 4;
-  const int blocks = p.rank >> 3;
-  const float scale = g.scales ? g.scales[slot / g.experts] : 1.0f;
-  const bool wide = (p.n & 3) == 0 && ((uintptr_t)p.y & 15) == 0 && ((uintptr_t)p.base & 15) == 0;
-  const int c0 = n0 + wave * (16 * NT);
-  if (c0 >= p.n) return;
 
-  for (int first = 0; first < tile.count; first += 16 * CT) {
-    // [hi | lo] of CT x 16 rows: lane (li, q) holds 8 values of row li
-    h8 v[CT][KC];
-    float back[CT];
-    int rows[CT];
+  // ---- the rows' v as [hi | lo]
+  constexpr int TPR = kLoraThreads / BM;                       // threads of a row
+  constexpr int UT = 4 * RC > TPR ? 4 * RC / TPR : 1;          // 8-rank units of a thread
+  const int units = p.rank >> 3;
+  {
+    const int m = threadIdx.x / TPR;
+    const int u0 = threadIdx.x % TPR;
+    const int row = tile.rows[m < count ? m : count - 1];
+    f4 f[UT][2];
+    float top = 0.0f;
 #pragma unroll
-    for (int t = 0; t < CT; ++t) {
-      const int at = first + t * 16 + li;
-      rows[t] = at < tile.count ? tile.rows[at] : -1;
-      const int row = at < tile.count ? rows[t] : tile.rows[tile.count - 1];
-      float f[KC][8];
-      float top = 0.0f;
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const int u = c * 4 + q;
-        f4 s0 = f4{0, 0, 0, 0}, s1 = s0;
-        if (u < 2 * blocks) {
-          auto vp = to_global(g.v) + p.v_offset + (size_t)row * p.rank_pad + (u < blocks ? u : u - blocks) * 8;
-          for (int s = 0; s < p.splits; ++s, vp += (size_t)g.rows * p.rank_pad) {
-            s0 += *(gptr<f4>)vp;
-            s1 += *(gptr<f4>)(vp + 4);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f[c][j] = j < 4 ? s0[j & 3] : s1[j & 3];
-          const float m = fabsf(f[c][j]);
-          if (m < __builtin_inff()) top = fmaxf(top, m);  // what is not finite stays so
+    for (int j = 0; j < UT; ++j) {
+      const int u = u0 + j * TPR;
+      f[j][0] = f[j][1] = f4{0, 0, 0, 0};
+      if (u < units) {
+        auto vp = to_global(g.v) + p.v_offset + (size_t)row * p.rank_pad + u * 8;
+        for (int s = 0; s < p.splits; ++s, vp += (size_t)g.rows * p.rank_pad) {
+          f[j][0] += *(gptr<f4>)vp;
+          f[j][1] += *(gptr<f4>)(vp + 4);
         }
       }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const int ex = __builtin_amdgcn_frexp_expf(top) - 15;
-      back[t] = ldexpf(1.0f, ex);
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const bool low = c * 4 + q >= blocks;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = ldexpf(f[c][j], -ex);
-          const half_t hi = (half_t)x;
-          const float rest = fabsf(x) < __builtin_inff() ? x - (float)hi : 0.0f;
-          v[t][c][j] = low ? (half_t)rest : hi;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(f[j][i >> 2][i & 3]);
+        if (a < __builtin_inff()) top = fmaxf(top, a);  // what is not finite stays so
       }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int nb = c0 + nt * 16;
-      if (nb >= p.n) break;
-      const int bn = nb + li < p.n ? nb + li : p.n - 1;
-      auto bp = to_global(p.b) + ((size_t)slot * p.n + bn) * p.rank;
-      f4 acc[CT];
+    for (int d = 1; d < TPR; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    const int ex = __builtin_amdgcn_frexp_expf(top) - 15;
+    if (u0 == 0) back[m] = ldexpf(1.0f, ex);
 #pragma unroll
-      for (int t = 0; t < CT; ++t) acc[t] = f4{0, 0, 0, 0};
+    for (int j = 0; j < UT; ++j) {
+      const int u = u0 + j * TPR;
+      if (u >= 4 * RC) break;
+      h8 hi, lo;
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const int u = c * 4 + q;
-        h8 b = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (u < 2 * blocks) b = *(gptr<h8>)(bp + (u < blocks ? u : u - blocks) * 8);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, v[t][c], acc[t], 0, 0, 0);
+      for (int i = 0; i < 8; ++i) {
+        const float x = ldexpf(f[j][i >> 2][i & 3], -ex);
+        hi[i] = (half_t)x;
+        lo[i] = (half_t)(fabsf(x) < __builtin_inff() ? x - (float)hi[i] : 0.0f);
       }
-      const int n = nb + q * 4;
+      *reinterpret_cast<h8*>(&vs[m * LD + u * 8]) = hi;
+      *reinterpret_cast<h8*>(&vs[m * LD + RC * 32 + u * 8]) = lo;
+    }
+  }
+  __syncthreads();
+
+  const int li = lane & 15;
+  const int q = lane >> 4;
+  const float scale = g.scales ? g.scales[slot / g.experts] : 1.0f;
+  for (int n0 = first + wave * 64; n0 < end; n0 += kLoraThreads) {
+    const int n = n0 + li * 4;
+    f4 o[CT][4];  // base: row 4 q + i of block c, columns n .. n + 3
 #pragma unroll
-      for (int t = 0; t < CT; ++t) {
-        if (rows[t] < 0 || n >= p.n) continue;
-        const size_t at = (size_t)rows[t] * p.n + n;
-        const f4 d = acc[t] * back[t];
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[c][i] = f4{0, 0, 0, 0};
+        const int at = c * 16 + q * 4 + i;
+        if (wide && p.base && at < count && n < end)
+          o[c][i] = *(gptr<f4>)(to_global(p.base) + (size_t)tile.rows[at] * p.n + n);
+      }
+    h8 b[RC][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int col = n + t < p.n ? n + t : p.n - 1;
+      auto bp = to_global(p.b) + ((size_t)slot * p.n + col) * p.rank;
+#pragma unroll
+      for (int c = 0; c < RC; ++c) {
+        const int u = c * 4 + q < units ? c * 4 + q : units - 1;
+        b[c][t] = *(gptr<h8>)(bp + u * 8);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      if (c * 16 >= count) break;
+      f4 acc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 2 * RC; ++k) {
+        const h8 v = *reinterpret_cast<const h8*>(&vs[(c * 16 + li) * LD + k * 32 + q * 8]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, b[k % RC][t], acc[t], 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = c * 16 + q * 4 + i;
+        if (at >= count || n >= end) continue;
+        const float undo = back[at];
+        float* y = p.y + (size_t)tile.rows[at] * p.n + n;
         if (wide) {
-          f4 o = p.base ? *(gptr<f4>)(to_global(p.base) + at) : f4{0, 0, 0, 0};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = fmaf(scale, d[j], o[j]);
-          *reinterpret_cast<f4*>(p.y + at) = o;
+          for (int t = 0; t < 4; ++t) o[c][i][t] = fmaf(scale, acc[t][i] * undo, o[c][i][t]);
+          *reinterpret_cast<f4*>(y) = o[c][i];
         } else {
+          const float* from = p.base ? p.base + (size_t)tile.rows[at] * p.n + n : nullptr;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (n + j < p.n) p.y[at + j] = fmaf(scale, d[j], p.base ? p.base[at + j] : 0.0f);
+          for (int t = 0; t < 4; ++t)
+            if (n + t < end) y[t] = fmaf(scale, acc[t][i] * undo, from ? from[t] : 0.0f);
         }
       }
     }
@@ -287,7 +398,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
 }
 
 // ------------------------------------------------------------------- route
-// Rows sorted by slot, and tiles of up to kLoraTileRows rows of one slot, as
+// Rows sorted by slot, and tiles of up to tile_rows rows of one slot, as
 // two launches over chunks of the rows (one if there is one chunk): count
 // the slots of each chunk, then place its rows behind those of the chunks
 // before it.  Buckets slots and slots + 1 hold the rows without adapter and
@@ -344,7 +455,7 @@ __global__ __launch_bounds__(kRouteThreads) void lora_place_kernel(LoraArgs g) {
     const int b = tid * per + i;
     const int n = b < buckets ? total[b] : 0;
     rows += n;
-    tiles += (n + kLoraTileRows - 1) / kLoraTileRows;
+    tiles += (n + g.tile_rows - 1) / g.tile_rows;
   }
   int row_sum = rows, tile_sum = tiles;
 #pragma unroll
@@ -373,8 +484,8 @@ __global__ __launch_bounds__(kRouteThreads) void lora_place_kernel(LoraArgs g) {
     cursor[b] += start;
     if (blockIdx.x == 0) {
       const int slot = b < g.slots ? b : b == g.slots ? kNone : kBad;
-      for (int j = 0; j < n; j += kLoraTileRows)
-        list[tile++] = LoraTile{slot, start + j, n - j < kLoraTileRows ? n - j : kLoraTileRows, 0};
+      for (int j = 0; j < n; j += g.tile_rows)
+        list[tile++] = LoraTile{slot, start + j, n - j < g.tile_rows ? n - j : g.tile_rows, 0};
     }
     start += n;
   }
@@ -390,16 +501,20 @@ __global__ __launch_bounds__(kRouteThreads) void lora_place_kernel(LoraArgs g) {
 
 static size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-static long lora_tiles(int rows, int slots) {
-  const long most = (long)rows / kLoraTileRows + slots + 2;  // a last tile of each bucket besides the whole ones
+static long lora_tiles(int rows, int tile_rows, int slots) {
+  const long most = (long)rows / tile_rows + slots + 2;  // a last tile of each bucket besides the whole ones
   return most < rows ? most : rows;
 }
 
-// Splits of k, chunks of the route and the places of everything in the
-// workspace; its size.
+// Tile height, splits of k, columns of a workgroup, chunks of the route and
+// the places of everything in the workspace; its size.
 size_t lora_layout(LoraArgs& g) {
   g.direct = g.rows <= kLoraDirectRows;
+  int rank = 0;
+  for (int i = 0; i < g.count; ++i) rank = g.p[i].rank > rank ? g.p[i].rank : rank;
+  g.tile_rows = g.direct || rank > 128 || g.rows < 24 * g.slots || g.rows < 1024 ? 16 : 64;
   size_t ints = 0;
+  g.tiles = g.rows;
   if (!g.direct) {
     const int buckets = g.slots + 2;
     g.chunks = kLoraCountWords / buckets;
@@ -408,25 +523,22 @@ size_t lora_layout(LoraArgs& g) {
     g.chunk = g.chunk < kLoraChunkMin ? kLoraChunkMin : g.chunk;
     if (g.rows <= kLoraOneChunk) g.chunk = g.rows;
     g.chunks = (g.rows + g.chunk - 1) / g.chunk;
-    g.tiles = lora_tiles(g.rows, g.slots);
+    g.tiles = lora_tiles(g.rows, g.tile_rows, g.slots);
     g.plan_tiles = up(kLoraPlanHeader + (size_t)g.rows, 4);
     g.plan_counts = g.plan_tiles + 4 * (size_t)g.tiles;
     ints = g.plan_counts + (g.chunks > 1 ? (size_t)g.chunks * buckets : 0);
   }
-  const size_t v0 = up(ints * 4, 256) / 4;  // in floats
-  size_t at = v0;
+  size_t at = up(ints * 4, 256) / 4;  // in floats
   for (int i = 0; i < g.count; ++i) {
     LoraProblem& p = g.p[i];
-    int splits;
-    if (g.direct) {
-      splits = (p.k + 511) / 512;
-    } else {
-      const long wgs = (long)(g.rows + kLoraTileRows - 1) / kLoraTileRows * ((p.rank + 63) / 64);
-      splits = (int)((512 + wgs - 1) / wgs);
-      if (splits > p.k / 512) splits = p.k / 512;
+    int splits = (p.k + 511) / 512;
+    if (g.tile_rows == 64) {
+      const long wgs = (long)(g.rows + 63) / 64 * ((p.rank + 63) / 64);
+      const long want = (512 + wgs - 1) / wgs;
+      splits = splits < want ? splits : (int)want;
     }
-    splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
-    const int unit = g.direct ? 256 : 64;
+    splits = splits > 8 ? 8 : splits;
+    const int unit = g.tile_rows == 16 ? 256 : 64;
     p.k_per_split = ((p.k + splits - 1) / splits + unit - 1) / unit * unit;
     p.splits = (p.k + p.k_per_split - 1) / p.k_per_split;
     p.rank_pad = (p.rank + 15) / 16 * 16;
@@ -436,8 +548,8 @@ size_t lora_layout(LoraArgs& g) {
   return at * sizeof(float);
 }
 
-template <bool ROUTED>
-static void launch_lora_products(const LoraArgs& g, hipStream_t st) {
+template <bool ROUTED, int BM>
+static void launch_lora_products(LoraArgs g, hipStream_t st) {
   int shrink_y = 1, rank = 1, n = 1;
   for (int i = 0; i < g.count; ++i) {
     const LoraProblem& p = g.p[i];
@@ -446,30 +558,38 @@ static void launch_lora_products(const LoraArgs& g, hipStream_t st) {
     rank = p.rank > rank ? p.rank : rank;
     n = p.n > n ? p.n : n;
   }
-  const unsigned tiles = (unsigned)(ROUTED ? g.tiles : g.rows);
+  const unsigned tiles = (unsigned)g.tiles;
   const dim3 block(kLoraThreads);
   const dim3 sg(tiles, shrink_y, g.count);
-  if (rank <= 16) hipLaunchKernelGGL((lora_shrink_kernel<ROUTED, 1>), sg, block, 0, st, g);
-  else if (rank <= 32) hipLaunchKernelGGL((lora_shrink_kernel<ROUTED, 2>), sg, block, 0, st, g);
-  else hipLaunchKernelGGL((lora_shrink_kernel<ROUTED, 4>), sg, block, 0, st, g);
-  constexpr int NT = ROUTED ? 4 : 1;
-  const dim3 eg(tiles, (n + 64 * NT - 1) / (64 * NT), g.count);
-  constexpr int C = ROUTED ? 4 : 1;
-  if (rank <= 16) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, 1, C, NT>), eg, block, 0, st, g);
-  else if (rank <= 32) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, 2, C, NT>), eg, block, 0, st, g);
-  else if (rank <= 64) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, 4, C, NT>), eg, block, 0, st, g);
-  else if (rank <= 128) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, 8, (C > 2 ? 2 : C), NT>), eg, block, 0, st, g);
-  else hipLaunchKernelGGL((lora_expand_kernel<ROUTED, 16, 1, NT>), eg, block, 0, st, g);
+  if constexpr (BM == 64) {
+    if (rank <= 16) hipLaunchKernelGGL(lora_shrink64_kernel<1>, sg, block, 0, st, g);
+    else if (rank <= 32) hipLaunchKernelGGL(lora_shrink64_kernel<2>, sg, block, 0, st, g);
+    else hipLaunchKernelGGL(lora_shrink64_kernel<4>, sg, block, 0, st, g);
+  } else {
+    if (rank <= 16) hipLaunchKernelGGL((lora_shrink16_kernel<ROUTED, 1>), sg, block, 0, st, g);
+    else if (rank <= 32) hipLaunchKernelGGL((lora_shrink16_kernel<ROUTED, 2>), sg, block, 0, st, g);
+    else hipLaunchKernelGGL((lora_shrink16_kernel<ROUTED, 4>), sg, block, 0, st, g);
+  }
+  // a workgroup's columns: 256, more where there are workgroups enough
+  const long blocks = (long)((n + 255) / 256) * ((g.rows + BM - 1) / BM);
+  const int turns = blocks >= 16384 ? 8 : blocks >= 8192 ? 4 : blocks >= 4096 ? 2 : 1;
+  g.columns = 256 * turns;
+  const dim3 eg(tiles, (n + g.columns - 1) / g.columns, g.count);
+  if (rank <= 32) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 1>), eg, block, 0, st, g);
+  else if (rank <= 64) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 2>), eg, block, 0, st, g);
+  else if (rank <= 128) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 4>), eg, block, 0, st, g);
+  else if constexpr (BM == 16) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 8>), eg, block, 0, st, g);
 }
 
 hipError_t launch_lora(const LoraArgs& g, hipStream_t st) {
   if (g.direct) {
-    launch_lora_products<false>(g, st);
+    launch_lora_products<false, 16>(g, st);
     return hipGetLastError();
   }
   if (g.chunks > 1) hipLaunchKernelGGL(lora_count_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);
   hipLaunchKernelGGL(lora_place_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);
-  launch_lora_products<true>(g, st);
+  if (g.tile_rows == 64) launch_lora_products<true, 64>(g, st);
+  else launch_lora_products<true, 16>(g, st);
   return hipGetLastError();
 }
 

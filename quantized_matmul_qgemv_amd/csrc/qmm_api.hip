@@ -80,8 +80,8 @@ int check_plan_size(const char* fn, size_t plan_bytes, int t, int top_k, int e) 
   return QMM_OK;
 }
 
-// Rows of one adapter call: pairs of a routed layer as in qmm_moe_route.
-constexpr long kMaxLoraRows = 0x7FFFFFFFL / 4;
+// Rows of one adapter call: tiles of 16, 256 threads each, within 2^32 threads.
+constexpr long kMaxLoraRows = 1 << 27;
 constexpr int kMaxLoraN = 1 << 21;  // column blocks of 64 in one grid dimension
 
 int check_lora_sizes(const char* fn, const qmm_lora_problem& q, int i) {

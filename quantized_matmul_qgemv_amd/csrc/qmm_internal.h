@@ -191,7 +191,6 @@ constexpr int kLoraMaxProblems = 8;
 constexpr int kLoraMaxSlots = 4096;     // adapters x experts: one LDS counter each
 constexpr int kLoraMaxRank = 256;
 constexpr int kLoraDirectRows = 256;    // rows up to which every workgroup finds its tile itself
-constexpr int kLoraTileRows = 64;       // rows of a sorted tile
 constexpr int kLoraPlanHeader = 8;      // words before the sorted rows
 constexpr int kLoraCountWords = 65536;  // chunks x buckets at most
 constexpr int kLoraChunkMin = 1024;     // rows a chunk at least
@@ -215,7 +214,7 @@ struct LoraArgs {
   int32_t* plan;               // the workspace, as words: header, sorted rows, tiles, counts
   size_t plan_tiles, plan_counts;
   int32_t count, rows, top_k, adapters, experts, slots;
-  int32_t direct, chunk, chunks;
+  int32_t direct, tile_rows, columns, chunk, chunks;
   int64_t tiles;  // most tiles that the rows can form
 };
 size_t lora_layout(LoraArgs& g);
