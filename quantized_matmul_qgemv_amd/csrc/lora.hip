@@ -21,6 +21,8 @@
 //
 // Every row is computed on its own (neither its tile nor its place in it
 // enters the sums), so results do not depend on scheduling.
+#include <stdlib.h>
+
 #include "qmm_device.h"
 #include "qmm_internal.h"
 
@@ -70,7 +72,7 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& g, int p, TileRows<BM>
   __syncthreads();
   const bool same = tid < g.rows && s == t.slot;
   const uint64_t m = __ballot(same);
-  if (lane == 0) masks[tid >> 6] = m;
+  if (lane == 0 && tid < kLoraDirectRows) masks[tid >> 6] = m;
   __syncthreads();
   int before = 0, total = 0, mine = 0;
 #pragma unroll
@@ -89,10 +91,18 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& g, int p, TileRows<BM>
   return true;
 }
 
-// Routed: tile `i` of the list.
+// Routed: the tile of workgroup i.  Workgroups are dealt round-robin to the
+// 8 XCDs (the grid's first dimension is a multiple of 8); each XCD takes a
+// run of the list, so that the tiles of a slot, next to each other there, read
+// its weights through one L2.
+constexpr int kXcds = 8;
 template <int BM>
 __device__ __forceinline__ bool read_tile(const LoraArgs& g, int i, TileRows<BM>& t) {
-  if (i >= g.plan[0]) return false;
+  const int tiles = g.plan[0];
+  const int run = (tiles + kXcds - 1) / kXcds;
+  if (i / kXcds >= run) return false;
+  i = i % kXcds * run + i / kXcds;
+  if (i >= tiles) return false;
   const int32_t* sorted = g.plan + kLoraPlanHeader;
   const LoraTile lt = reinterpret_cast<const LoraTile*>(g.plan + g.plan_tiles)[i];
   if (threadIdx.x < BM && threadIdx.x < lt.rows) t.rows[threadIdx.x] = sorted[lt.start + threadIdx.x];
@@ -202,44 +212,52 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink64_kernel(LoraArgs g)
     const int r = r0 + sr + 32 * j < p.rank ? r0 + sr + 32 * j : p.rank - 1;
     ap[j] = to_global(p.a) + ((size_t)tile.slot * p.rank + r) * p.k + sc;
   }
-  u32x4 xr[XL], ar[AL];
-  auto fetch = [&](int k) {
+  u32x4 xr[2][XL], ar[2][AL];  // two steps in flight
+  const int kbeg = split * p.k_per_split;
+  const int kend = kbeg + p.k_per_split < p.k ? kbeg + p.k_per_split : p.k;
+  auto fetch = [&](int set, int k) {
+    if (k >= kend) return;
 #pragma unroll
-    for (int j = 0; j < XL; ++j) xr[j] = *(gptr<u32x4>)(xp[j] + k);
+    for (int j = 0; j < XL; ++j) xr[set][j] = *(gptr<u32x4>)(xp[j] + k);
 #pragma unroll
-    for (int j = 0; j < AL; ++j) ar[j] = *(gptr<u32x4>)(ap[j] + k);
+    for (int j = 0; j < AL; ++j) ar[set][j] = *(gptr<u32x4>)(ap[j] + k);
   };
-  auto stage = [&](int buf) {
+  auto stage = [&](int set, int buf) {
 #pragma unroll
-    for (int j = 0; j < XL; ++j) *reinterpret_cast<u32x4*>(&xs[buf][(sr + 32 * j) * kStage + sc]) = xr[j];
+    for (int j = 0; j < XL; ++j) *reinterpret_cast<u32x4*>(&xs[buf][(sr + 32 * j) * kStage + sc]) = xr[set][j];
 #pragma unroll
     for (int j = 0; j < AL; ++j)
-      if (RT > 1 || sr < 16) *reinterpret_cast<u32x4*>(&as[buf][(sr + 32 * j) * kStage + sc]) = ar[j];
+      if (RT > 1 || sr < 16) *reinterpret_cast<u32x4*>(&as[buf][(sr + 32 * j) * kStage + sc]) = ar[set][j];
   };
   f4 acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-  const int kbeg = split * p.k_per_split;
-  const int kend = kbeg + p.k_per_split < p.k ? kbeg + p.k_per_split : p.k;
-  fetch(kbeg);
-  stage(0);
-  int buf = 0;
-  for (int k = kbeg; k < kend; k += 64, buf ^= 1) {
-    __syncthreads();
-    const bool more = k + 64 < kend;
-    if (more) fetch(k + 64);
-    if (wave * 16 < count) {
+  auto multiply = [&](int buf) {
+    if (wave * 16 >= count) return;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const h8 x = *reinterpret_cast<const h8*>(&xs[buf][(wave * 16 + li) * kStage + h * 32 + q * 8]);
+    for (int h = 0; h < 2; ++h) {
+      const h8 x = *reinterpret_cast<const h8*>(&xs[buf][(wave * 16 + li) * kStage + h * 32 + q * 8]);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const h8 a = *reinterpret_cast<const h8*>(&as[buf][(i * 16 + li) * kStage + h * 32 + q * 8]);
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x, acc[i], 0, 0, 0);
-        }
+      for (int i = 0; i < RT; ++i) {
+        const h8 a = *reinterpret_cast<const h8*>(&as[buf][(i * 16 + li) * kStage + h * 32 + q * 8]);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, x, acc[i], 0, 0, 0);
       }
     }
-    if (more) stage(buf ^ 1);
+  };
+  fetch(0, kbeg);
+  fetch(1, kbeg + 64);
+  stage(0, 0);
+  fetch(0, kbeg + 128);
+  for (int k = kbeg; k < kend; k += 128) {
+    __syncthreads();
+    if (k + 64 < kend) stage(1, 1);
+    fetch(1, k + 192);
+    multiply(0);
+    if (k + 64 >= kend) break;
+    __syncthreads();
+    if (k + 128 < kend) stage(0, 0);
+    fetch(0, k + 256);
+    multiply(1);
   }
   const int at = wave * 16 + li;
   if (at >= count) return;
@@ -250,123 +268,46 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink64_kernel(LoraArgs g)
 }
 
 // ------------------------------------------------------------------ expand
-// One workgroup: a tile's BM rows and a range of columns, 64 for each wave at
-// a time.  First all threads sum the rows' partials and leave [hi | lo] in
-// LDS (ranks padded with zeros to 32 * RC).  Then rows x columns on the
-// matrix cores, D[row][column]: block t of a wave's four takes the columns
-// 4 j + t, j = 0 .. 15, so that a lane ends with four neighbouring columns of
-// a row and 16 lanes load base and store y by 256 bytes.
-template <bool ROUTED, int BM, int RC>
-__global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
-  constexpr int CT = BM / 16;
-  constexpr int LD = 2 * RC * 32 + 8;  // halves from row to row in LDS
-  __shared__ TileRows<BM> tile;
-  __shared__ uint64_t masks[kLoraDirectRows / 64];
-  __shared__ __attribute__((aligned(16))) half_t vs[BM * LD];
-  __shared__ float back[BM];  // what undoes a row's power of two
-  const LoraProblem& p = g.p[blockIdx.z];
-  const int first = blockIdx.y * g.columns;
-  if (first >= p.n) return;
-  if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile(g, blockIdx.x, tile, masks))) return;
-  const int slot = tile.slot;
-  const int count = tile.count;
-  const int end = first + g.columns < p.n ? first + g.columns : p.n;
-  const bool wide = (p.n & 3) == 0 && ((uintptr_t)p.y & 15) == 0 && ((uintptr_t)p.base & 15) == 0;
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  if (slot < 0) {
-    if (slot == kNone && p.base == p.y) return;
-    for (int i = wave; i < count; i += kLoraThreads / 64) {
-      const size_t at = (size_t)tile.rows[i] * p.n;
-      const float fill = slot == kBad ? __builtin_nanf("") : 0.0f;
-      const float* from = slot == kBad ? nullptr : p.base;
-      if (wide) {
-        for (int n = first + lane * 4; n < end; n += 256)
-          *reinterpret_cast<f4*>(p.y + at + n) = from ? *(gptr<f4>)(to_global(from) + at + n) : f4{fill, fill, fill, fill};
-      } else {
-        for (int n = first + lane; n < end; n += 64) p.y[at + n] = from ? from[at + n] : fill;
-      }
-    }
-    return;
-  }
+// The second product of a tile's BM rows and a workgroup's columns, 64 for
+// each wave at a time: rows x columns on the matrix cores, D[row][column].
+// Block t of a wave's four takes the columns 4 j + t, j = 0 .. 15, so that a
+// lane ends with four neighbouring columns of a row and 16 lanes load base
+// and store y by 256 bytes.  RC: ranks in steps of 32.
+template <int BM, int RC>
+struct Columns {
+  static constexpr int CT = BM / 16;
+  static constexpr int LD = 2 * RC * 32 + 8;  // halves from row to row of [hi | lo] in LDS
+  f4 o[CT][4];  // base: row 4 q + i of block c, four columns
+  h8 b[RC][4];
 
-  // ---- the rows' v as [hi | lo]
-  constexpr int TPR = kLoraThreads / BM;                       // threads of a row
-  constexpr int UT = 4 * RC > TPR ? 4 * RC / TPR : 1;          // 8-rank units of a thread
-  const int units = p.rank >> 3;
-  {
-    const int m = threadIdx.x / TPR;
-    const int u0 = threadIdx.x % TPR;
-    const int row = tile.rows[m < count ? m : count - 1];
-    f4 f[UT][2];
-    float top = 0.0f;
+  __device__ __forceinline__ void load(const LoraProblem& p, const TileRows<BM>& tile, int n, int end, bool wide) {
+    const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
-    for (int j = 0; j < UT; ++j) {
-      const int u = u0 + j * TPR;
-      f[j][0] = f[j][1] = f4{0, 0, 0, 0};
-      if (u < units) {
-        auto vp = to_global(g.v) + p.v_offset + (size_t)row * p.rank_pad + u * 8;
-        for (int s = 0; s < p.splits; ++s, vp += (size_t)g.rows * p.rank_pad) {
-          f[j][0] += *(gptr<f4>)vp;
-          f[j][1] += *(gptr<f4>)(vp + 4);
-        }
-      }
+    for (int t = 0; t < 4; ++t) {
+      const int col = n + t < p.n ? n + t : p.n - 1;
+      auto bp = to_global(p.b) + ((size_t)tile.slot * p.n + col) * p.rank;
+      const int units = p.rank >> 3;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(f[j][i >> 2][i & 3]);
-        if (a < __builtin_inff()) top = fmaxf(top, a);  // what is not finite stays so
-      }
+      for (int c = 0; c < RC; ++c) b[c][t] = *(gptr<h8>)(bp + (c * 4 + q < units ? c * 4 + q : units - 1) * 8);
     }
-#pragma unroll
-    for (int d = 1; d < TPR; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    const int ex = __builtin_amdgcn_frexp_expf(top) - 15;
-    if (u0 == 0) back[m] = ldexpf(1.0f, ex);
-#pragma unroll
-    for (int j = 0; j < UT; ++j) {
-      const int u = u0 + j * TPR;
-      if (u >= 4 * RC) break;
-      h8 hi, lo;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = ldexpf(f[j][i >> 2][i & 3], -ex);
-        hi[i] = (half_t)x;
-        lo[i] = (half_t)(fabsf(x) < __builtin_inff() ? x - (float)hi[i] : 0.0f);
-      }
-      *reinterpret_cast<h8*>(&vs[m * LD + u * 8]) = hi;
-      *reinterpret_cast<h8*>(&vs[m * LD + RC * 32 + u * 8]) = lo;
-    }
-  }
-  __syncthreads();
-
-  const int li = lane & 15;
-  const int q = lane >> 4;
-  const float scale = g.scales ? g.scales[slot / g.experts] : 1.0f;
-  for (int n0 = first + wave * 64; n0 < end; n0 += kLoraThreads) {
-    const int n = n0 + li * 4;
-    f4 o[CT][4];  // base: row 4 q + i of block c, columns n .. n + 3
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         o[c][i] = f4{0, 0, 0, 0};
         const int at = c * 16 + q * 4 + i;
-        if (wide && p.base && at < count && n < end)
+        if (wide && p.base && at < tile.count && n < end)
           o[c][i] = *(gptr<f4>)(to_global(p.base) + (size_t)tile.rows[at] * p.n + n);
       }
-    h8 b[RC][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int col = n + t < p.n ? n + t : p.n - 1;
-      auto bp = to_global(p.b) + ((size_t)slot * p.n + col) * p.rank;
-#pragma unroll
-      for (int c = 0; c < RC; ++c) {
-        const int u = c * 4 + q < units ? c * 4 + q : units - 1;
-        b[c][t] = *(gptr<h8>)(bp + u * 8);
-      }
-    }
+  }
+
+  __device__ __forceinline__ void finish(const LoraProblem& p, const TileRows<BM>& tile, int n, int end, bool wide,
+                                         const half_t* vs, const float* back, float scale) {
+    const int li = threadIdx.x & 15;
+    const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      if (c * 16 >= count) break;
+      if (c * 16 >= tile.count) break;
       f4 acc[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[t] = f4{0, 0, 0, 0};
@@ -379,7 +320,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int at = c * 16 + q * 4 + i;
-        if (at >= count || n >= end) continue;
+        if (at >= tile.count || n >= end) continue;
         const float undo = back[at];
         float* y = p.y + (size_t)tile.rows[at] * p.n + n;
         if (wide) {
@@ -395,6 +336,193 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
       }
     }
   }
+};
+
+// Rows of a tile without weights of their own: base as it is, or NaN.
+template <int BM>
+__device__ __forceinline__ void plain_rows(const LoraProblem& p, const TileRows<BM>& tile, int first, int end, bool wide) {
+  if (tile.slot == kNone && p.base == p.y) return;
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x >> 6; i < tile.count; i += blockDim.x >> 6) {
+    const size_t at = (size_t)tile.rows[i] * p.n;
+    const float fill = tile.slot == kBad ? __builtin_nanf("") : 0.0f;
+    const float* from = tile.slot == kBad ? nullptr : p.base;
+    if (wide) {
+      for (int n = first + lane * 4; n < end; n += 256)
+        *reinterpret_cast<f4*>(p.y + at + n) = from ? *(gptr<f4>)(to_global(from) + at + n) : f4{fill, fill, fill, fill};
+    } else {
+      for (int n = first + lane; n < end; n += 64) p.y[at + n] = from ? from[at + n] : fill;
+    }
+  }
+}
+
+// v of row m, of which this thread (u0 of TPR neighbours) holds UT units of 8
+// ranks (f[j]: unit u0 + j * TPR), into LDS as [hi | lo].
+template <int RC, int LD, int TPR, int UT>
+__device__ __forceinline__ void split_row(const f4 (&f)[UT][2], int m, int u0, half_t* vs, float* back) {
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < UT; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(f[j][i >> 2][i & 3]);
+      if (a < __builtin_inff()) top = fmaxf(top, a);  // what is not finite stays so
+    }
+#pragma unroll
+  for (int d = 1; d < TPR; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  const int ex = __builtin_amdgcn_frexp_expf(top) - 15;
+  if (u0 == 0) back[m] = ldexpf(1.0f, ex);
+#pragma unroll
+  for (int j = 0; j < UT; ++j) {
+    const int u = u0 + j * TPR;
+    if (u >= 4 * RC) break;
+    h8 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = ldexpf(f[j][i >> 2][i & 3], -ex);
+      hi[i] = (half_t)x;
+      lo[i] = (half_t)(fabsf(x) < __builtin_inff() ? x - (float)hi[i] : 0.0f);
+    }
+    *reinterpret_cast<h8*>(&vs[m * LD + u * 8]) = hi;
+    *reinterpret_cast<h8*>(&vs[m * LD + RC * 32 + u * 8]) = lo;
+  }
+}
+
+__device__ __forceinline__ bool wide_columns(const LoraProblem& p) {
+  return (p.n & 3) == 0 && ((uintptr_t)p.y & 15) == 0 && ((uintptr_t)p.base & 15) == 0;
+}
+
+template <bool ROUTED, int BM, int RC>
+__global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
+  using C = Columns<BM, RC>;
+  __shared__ TileRows<BM> tile;
+  __shared__ uint64_t masks[kLoraDirectRows / 64];
+  __shared__ __attribute__((aligned(16))) half_t vs[BM * C::LD];
+  __shared__ float back[BM];  // what undoes a row's power of two
+  const LoraProblem& p = g.p[blockIdx.z];
+  const int first = blockIdx.y * g.columns;
+  if (first >= p.n) return;
+  if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile(g, blockIdx.x, tile, masks))) return;
+  const int end = first + g.columns < p.n ? first + g.columns : p.n;
+  const bool wide = wide_columns(p);
+  if (tile.slot < 0) {
+    plain_rows(p, tile, first, end, wide);
+    return;
+  }
+  const int step = (threadIdx.x >> 6) * 64 + (threadIdx.x & 15) * 4;
+  C cols;
+  cols.load(p, tile, first + step, end, wide);  // in flight while v is formed
+
+  constexpr int TPR = kLoraThreads / BM;               // threads of a row
+  constexpr int UT = 4 * RC > TPR ? 4 * RC / TPR : 1;  // units of a thread
+  const int m = threadIdx.x / TPR;
+  const int u0 = threadIdx.x % TPR;
+  const int row = tile.rows[m < tile.count ? m : tile.count - 1];
+  f4 f[UT][2];
+#pragma unroll
+  for (int j = 0; j < UT; ++j) {
+    f[j][0] = f[j][1] = f4{0, 0, 0, 0};
+    if ((u0 + j * TPR) * 8 < p.rank) {
+      auto vp = to_global(g.v) + p.v_offset + (size_t)row * p.rank_pad + (u0 + j * TPR) * 8;
+      for (int s = 0; s < p.splits; ++s, vp += (size_t)g.rows * p.rank_pad) {
+        f[j][0] += *(gptr<f4>)vp;
+        f[j][1] += *(gptr<f4>)(vp + 4);
+      }
+    }
+  }
+  split_row<RC, C::LD, TPR, UT>(f, m, u0, vs, back);
+  __syncthreads();
+
+  const float scale = g.scales ? g.scales[tile.slot / g.experts] : 1.0f;
+  for (int n = first;;) {
+    cols.finish(p, tile, n + step, end, wide, vs, back, scale);
+    n += kLoraThreads;
+    if (n >= end) break;
+    cols.load(p, tile, n + step, end, wide);
+  }
+}
+
+// ------------------------------------------------------------------- fused
+// Few rows, a small A: both products in one launch.  Every workgroup forms
+// its tile's v itself (the other workgroups of the tile read the same A from
+// L2, on the same XCD where the rows are a multiple of 8), its eight waves
+// taking turns at 64 values of k, then goes on to its columns, whose first
+// loads it has issued before.
+constexpr int kFusedThreads = 512;
+template <int RT>
+__global__ __launch_bounds__(kFusedThreads) void lora_fused_kernel(LoraArgs g) {
+  constexpr int RC = (RT + 1) / 2;
+  constexpr int WAVES = kFusedThreads / 64;
+  using C = Columns<16, RC>;
+  __shared__ TileRows<16> tile;
+  __shared__ uint64_t masks[kLoraDirectRows / 64];
+  __shared__ f4 part[WAVES][RT][64];
+  __shared__ __attribute__((aligned(16))) half_t vs[16 * C::LD];
+  __shared__ float back[16];
+  const LoraProblem& p = g.p[blockIdx.z];
+  const int first = blockIdx.y * g.columns;
+  if (first >= p.n) return;
+  if (!find_tile(g, blockIdx.x, tile, masks)) return;
+  const int end = first + g.columns < p.n ? first + g.columns : p.n;
+  const bool wide = wide_columns(p);
+  if (tile.slot < 0) {
+    plain_rows(p, tile, first, end, wide);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int li = lane & 15;
+  const int q = lane >> 4;
+  const int row = tile.rows[li < tile.count ? li : tile.count - 1];
+  auto xp = to_global(p.x) + (size_t)lora_x_row(g, p, row) * p.k + q * 16;
+  gptr<uint16_t> ap[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = i * 16 + li < p.rank ? i * 16 + li : p.rank - 1;
+    ap[i] = to_global(p.a) + ((size_t)tile.slot * p.rank + r) * p.k + q * 16;
+  }
+  f4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
+#pragma unroll 4
+  for (int k = wave * 64; k < p.k; k += WAVES * 64) {
+    const h8 x0 = *(gptr<h8>)(xp + k), x1 = *(gptr<h8>)(xp + k + 8);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const h8 a0 = *(gptr<h8>)(ap[i] + k), a1 = *(gptr<h8>)(ap[i] + k + 8);
+      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, x0, acc[i], 0, 0, 0);
+      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, x1, acc[i], 0, 0, 0);
+    }
+  }
+  const int step = wave * 64 + li * 4;
+  C cols;
+  cols.load(p, tile, first + step, end, wide);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  // thread (m, u0 of 32): the 8 ranks of unit u0 are two quads of a block's 16
+  constexpr int TPR = kFusedThreads / 16;
+  const int m = threadIdx.x / TPR;
+  const int u0 = threadIdx.x % TPR;
+  f4 f[1][2];
+  f[0][0] = f[0][1] = f4{0, 0, 0, 0};
+  if (u0 * 8 < p.rank) {
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      f[0][0] += part[w][u0 >> 1][(u0 & 1) * 32 + m];
+      f[0][1] += part[w][u0 >> 1][(u0 & 1) * 32 + 16 + m];
+    }
+  }
+  split_row<RC, C::LD, TPR, 1>(f, m, u0, vs, back);
+  __syncthreads();
+
+  const float scale = g.scales ? g.scales[tile.slot / g.experts] : 1.0f;
+  for (int n = first;;) {
+    cols.finish(p, tile, n + step, end, wide, vs, back, scale);
+    n += kFusedThreads;
+    if (n >= end) break;
+    cols.load(p, tile, n + step, end, wide);
+  }
 }
 
 // ------------------------------------------------------------------- route
@@ -404,11 +532,38 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
 // before it.  Buckets slots and slots + 1 hold the rows without adapter and
 // those with bad ids.
 constexpr int kRouteThreads = 1024;
+static_assert(kLoraOneChunk == 4 * kRouteThreads, "one chunk's rows are four of each thread");
 constexpr int kLoraBuckets = kLoraMaxSlots + 2;
 
-__device__ __forceinline__ int lora_bucket(const LoraArgs& g, int p) {
-  const int s = lora_slot(g, p);
-  return s >= 0 ? s : s == kNone ? g.slots : g.slots + 1;
+constexpr int kBatch = 4;  // rows of a thread whose ids are loaded together
+
+// The buckets of rows p, p + kRouteThreads, ...; -1 from row `end` on.
+__device__ __forceinline__ void lora_buckets(const LoraArgs& g, int p, int end, int (&b)[kBatch]) {
+  int a[kBatch], e[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int at = p + i * kRouteThreads < end ? p + i * kRouteThreads : end - 1;
+    a[i] = g.adapter_ids[g.top_k == 1 ? at : at / g.top_k];
+    e[i] = g.expert_ids ? g.expert_ids[at] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const bool ok = a[i] >= 0 && a[i] < g.adapters && e[i] >= 0 && e[i] < g.experts;
+    b[i] = p + i * kRouteThreads >= end ? -1 : ok ? a[i] * g.experts + e[i] : a[i] == -1 ? g.slots : g.slots + 1;
+  }
+}
+
+// Adds one to the row's counter and returns what it was.  A wave whose rows
+// all share a bucket, as in a prompt, does so once.
+__device__ __forceinline__ int lora_take(int32_t* counters, int b) {
+  const int first = __builtin_amdgcn_readfirstlane(b);
+  if (__all(b == first)) {
+    int at = 0;
+    const int lane = threadIdx.x & 63;
+    if (lane == 0 && first >= 0) at = atomicAdd(&counters[first], 64);
+    return __builtin_amdgcn_readfirstlane(at) + lane;
+  }
+  return b >= 0 ? atomicAdd(&counters[b], 1) : 0;
 }
 
 __global__ __launch_bounds__(kRouteThreads) void lora_count_kernel(LoraArgs g) {
@@ -418,7 +573,12 @@ __global__ __launch_bounds__(kRouteThreads) void lora_count_kernel(LoraArgs g) {
   __syncthreads();
   const int p0 = blockIdx.x * g.chunk;
   const int p1 = p0 + g.chunk < g.rows ? p0 + g.chunk : g.rows;
-  for (int p = p0 + threadIdx.x; p < p1; p += kRouteThreads) atomicAdd(&h[lora_bucket(g, p)], 1);
+  for (int base = p0; base < p1; base += kBatch * kRouteThreads) {
+    int b[kBatch];
+    lora_buckets(g, base + threadIdx.x, p1, b);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) lora_take(h, b[i]);
+  }
   __syncthreads();
   int32_t* out = g.plan + g.plan_counts + (size_t)blockIdx.x * buckets;
   for (int i = threadIdx.x; i < buckets; i += kRouteThreads) out[i] = h[i];
@@ -432,19 +592,32 @@ __global__ __launch_bounds__(kRouteThreads) void lora_place_kernel(LoraArgs g) {
   const int lane = tid & 63;
   const int wave = tid >> 6;
   const int buckets = g.slots + 2;
+  const int p0 = blockIdx.x * g.chunk;
+  const int p1 = p0 + g.chunk < g.rows ? p0 + g.chunk : g.rows;
+  // the chunk's first rows stay in registers: all of them where there is one
+  // chunk (kLoraOneChunk rows), whose counting also places them
+  int b[kBatch], at[kBatch];
+  lora_buckets(g, p0 + tid, p1, b);
   for (int i = tid; i < buckets; i += kRouteThreads) total[i] = cursor[i] = 0;
   __syncthreads();
   if (g.chunks == 1) {
-    for (int p = tid; p < g.rows; p += kRouteThreads) atomicAdd(&total[lora_bucket(g, p)], 1);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) at[i] = lora_take(total, b[i]);
   } else {
     const int32_t* counts = g.plan + g.plan_counts;
-    for (int i = tid; i < buckets * g.chunks; i += kRouteThreads) {
-      const int n = counts[i];
-      if (n == 0) continue;
-      const int c = i / buckets;
-      const int b = i - c * buckets;
-      atomicAdd(&total[b], n);
-      if (c < (int)blockIdx.x) atomicAdd(&cursor[b], n);
+    const int words = buckets * g.chunks;
+    for (int base = tid; base < words; base += kBatch * kRouteThreads) {
+      int n[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) n[i] = base + i * kRouteThreads < words ? counts[base + i * kRouteThreads] : 0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (n[i] == 0) continue;
+        const int c = (base + i * kRouteThreads) / buckets;
+        const int k = base + i * kRouteThreads - c * buckets;
+        atomicAdd(&total[k], n[i]);
+        if (c < (int)blockIdx.x) atomicAdd(&cursor[k], n[i]);
+      }
     }
   }
   __syncthreads();
@@ -491,10 +664,21 @@ __global__ __launch_bounds__(kRouteThreads) void lora_place_kernel(LoraArgs g) {
   }
   if (blockIdx.x == 0 && tid == kRouteThreads - 1) g.plan[0] = tile;
   __syncthreads();
-  const int p0 = blockIdx.x * g.chunk;
-  const int p1 = p0 + g.chunk < g.rows ? p0 + g.chunk : g.rows;
   int32_t* sorted = g.plan + kLoraPlanHeader;
-  for (int p = p0 + tid; p < p1; p += kRouteThreads) sorted[atomicAdd(&cursor[lora_bucket(g, p)], 1)] = p;
+  if (g.chunks == 1) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (b[i] >= 0) sorted[cursor[b[i]] + at[i]] = p0 + tid + i * kRouteThreads;
+    return;
+  }
+  for (int base = p0; base < p1; base += kBatch * kRouteThreads) {
+    if (base > p0) lora_buckets(g, base + tid, p1, b);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int to = lora_take(cursor, b[i]);
+      if (b[i] >= 0) sorted[to] = base + tid + i * kRouteThreads;
+    }
+  }
 }
 
 // -------------------------------------------------------------------- host
@@ -534,7 +718,8 @@ size_t lora_layout(LoraArgs& g) {
     int splits = (p.k + 511) / 512;
     if (g.tile_rows == 64) {
       const long wgs = (long)(g.rows + 63) / 64 * ((p.rank + 63) / 64);
-      const long want = (512 + wgs - 1) / wgs;
+      static const long tgt = getenv("QMM_LORA_S") ? atol(getenv("QMM_LORA_S")) : 512;
+      const long want = (tgt + wgs - 1) / wgs;
       splits = splits < want ? splits : (int)want;
     }
     splits = splits > 8 ? 8 : splits;
@@ -558,7 +743,7 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
     rank = p.rank > rank ? p.rank : rank;
     n = p.n > n ? p.n : n;
   }
-  const unsigned tiles = (unsigned)g.tiles;
+  const unsigned tiles = (unsigned)(ROUTED ? up(g.tiles, kXcds) : g.tiles);
   const dim3 block(kLoraThreads);
   const dim3 sg(tiles, shrink_y, g.count);
   if constexpr (BM == 64) {
@@ -581,9 +766,37 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
   else if constexpr (BM == 16) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 8>), eg, block, 0, st, g);
 }
 
+// One launch where every problem's A is small enough to be read again by
+// each workgroup of a tile.
+static bool lora_fused(const LoraArgs& g) {
+  static const long most = getenv("QMM_LORA_FUSED") ? atol(getenv("QMM_LORA_FUSED")) : 192;
+  for (int i = 0; i < g.count; ++i)
+    if (g.p[i].rank > 64 || (long)g.p[i].rank_pad * g.p[i].k * 2 > most * 1024) return false;
+  return true;
+}
+
+static void launch_lora_fused(LoraArgs g, hipStream_t st) {
+  int rank = 1, n = 1;
+  long columns = 0;  // of all problems
+  for (int i = 0; i < g.count; ++i) {
+    rank = g.p[i].rank > rank ? g.p[i].rank : rank;
+    n = g.p[i].n > n ? g.p[i].n : n;
+    columns += g.p[i].n;
+  }
+  static const long target = getenv("QMM_LORA_WGS") ? atol(getenv("QMM_LORA_WGS")) : 512;
+  long per = (columns * g.rows + target - 1) / target;
+  per = (per + 511) / 512 * 512;
+  g.columns = (int)(per < 512 ? 512 : per > 4096 ? 4096 : per);
+  const dim3 grid(g.rows, (n + g.columns - 1) / g.columns, g.count), block(kFusedThreads);
+  if (rank <= 16) hipLaunchKernelGGL(lora_fused_kernel<1>, grid, block, 0, st, g);
+  else if (rank <= 32) hipLaunchKernelGGL(lora_fused_kernel<2>, grid, block, 0, st, g);
+  else hipLaunchKernelGGL(lora_fused_kernel<4>, grid, block, 0, st, g);
+}
+
 hipError_t launch_lora(const LoraArgs& g, hipStream_t st) {
   if (g.direct) {
-    launch_lora_products<false, 16>(g, st);
+    if (lora_fused(g)) launch_lora_fused(g, st);
+    else launch_lora_products<false, 16>(g, st);
     return hipGetLastError();
   }
   if (g.chunks > 1) hipLaunchKernelGGL(lora_count_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);
