@@ -62,21 +62,22 @@ struct TileRows {
 };
 
 // Direct: the workgroup of row p owns the tile that starts at p, if an equal
-// number of rows with p's slot, a multiple of BM, comes before it.
-template <int BM>
-__device__ __forceinline__ bool find_tile(const LoraArgs& g, int p, TileRows<BM>& t, uint64_t* masks) {
+// number of rows with p's slot, a multiple of BM, comes before it.  The
+// workgroup has a thread for every row, up to ROWS.
+template <int ROWS, int BM>
+__device__ __forceinline__ bool find_tile(const LoraArgs& g, int p, TileRows<BM>& t) {
+  __shared__ uint64_t masks[ROWS / 64];
   const int tid = threadIdx.x;
-  const int lane = tid & 63;
   const int s = tid < g.rows ? lora_slot(g, tid) : 0;
   if (tid == p) t.slot = s;
   __syncthreads();
   const bool same = tid < g.rows && s == t.slot;
   const uint64_t m = __ballot(same);
-  if (lane == 0 && tid < kLoraDirectRows) masks[tid >> 6] = m;
+  if ((tid & 63) == 0) masks[tid >> 6] = m;
   __syncthreads();
   int before = 0, total = 0, mine = 0;
 #pragma unroll
-  for (int w = 0; w < kLoraDirectRows / 64; ++w) {
+  for (int w = 0; w < ROWS / 64; ++w) {
     const uint64_t b = masks[w];
     const int lo = p - w * 64, li = tid - w * 64;
     before += __popcll(lo >= 64 ? b : lo > 0 ? b & ((1ull << lo) - 1) : 0);
@@ -84,9 +85,8 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& g, int p, TileRows<BM>
     total += __popcll(b);
   }
   if (before % BM != 0) return false;
-  const int count = total - before < BM ? total - before : BM;
   if (same && mine >= before && mine < before + BM) t.rows[mine - before] = tid;
-  if (tid == 0) t.count = count;
+  if (tid == 0) t.count = total - before < BM ? total - before : BM;
   __syncthreads();
   return true;
 }
@@ -124,14 +124,13 @@ __device__ __forceinline__ bool read_tile(const LoraArgs& g, int i, TileRows<BM>
 template <bool ROUTED, int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink16_kernel(LoraArgs g) {
   __shared__ TileRows<16> tile;
-  __shared__ uint64_t masks[kLoraDirectRows / 64];
   __shared__ f4 part[3][RT][64];
   const LoraProblem& p = g.p[blockIdx.z];
   const int chunks = (p.rank + 63) >> 6;
   const int split = blockIdx.y / chunks;
   const int r0 = (blockIdx.y - split * chunks) * 64;
   if (split >= p.splits) return;
-  if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile(g, blockIdx.x, tile, masks))) return;
+  if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile<kLoraThreads>(g, blockIdx.x, tile))) return;
   if (tile.slot < 0) return;
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -297,7 +296,7 @@ struct Columns {
         o[c][i] = f4{0, 0, 0, 0};
         const int at = c * 16 + q * 4 + i;
         if (wide && p.base && at < tile.count && n < end)
-          o[c][i] = *(gptr<f4>)(to_global(p.base) + (size_t)tile.rows[at] * p.n + n);
+          o[c][i] = __builtin_nontemporal_load((gptr<f4>)(to_global(p.base) + (size_t)tile.rows[at] * p.n + n));
       }
   }
 
@@ -326,7 +325,7 @@ struct Columns {
         if (wide) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) o[c][i][t] = fmaf(scale, acc[t][i] * undo, o[c][i][t]);
-          *reinterpret_cast<f4*>(y) = o[c][i];
+          __builtin_nontemporal_store(o[c][i], (gptr_mut<f4>)to_global_mut(y));
         } else {
           const float* from = p.base ? p.base + (size_t)tile.rows[at] * p.n + n : nullptr;
 #pragma unroll
@@ -348,8 +347,17 @@ __device__ __forceinline__ void plain_rows(const LoraProblem& p, const TileRows<
     const float fill = tile.slot == kBad ? __builtin_nanf("") : 0.0f;
     const float* from = tile.slot == kBad ? nullptr : p.base;
     if (wide) {
-      for (int n = first + lane * 4; n < end; n += 256)
-        *reinterpret_cast<f4*>(p.y + at + n) = from ? *(gptr<f4>)(to_global(from) + at + n) : f4{fill, fill, fill, fill};
+      for (int n0 = first + lane * 4; n0 < end; n0 += 256 * 8) {  // eight loads in flight
+        f4 o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j] = f4{fill, fill, fill, fill};
+          if (from && n0 + j * 256 < end) o[j] = *(gptr<f4>)(to_global(from) + at + n0 + j * 256);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n0 + j * 256 < end) *reinterpret_cast<f4*>(p.y + at + n0 + j * 256) = o[j];
+      }
     } else {
       for (int n = first + lane; n < end; n += 64) p.y[at + n] = from ? from[at + n] : fill;
     }
@@ -396,13 +404,12 @@ template <bool ROUTED, int BM, int RC>
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
   using C = Columns<BM, RC>;
   __shared__ TileRows<BM> tile;
-  __shared__ uint64_t masks[kLoraDirectRows / 64];
   __shared__ __attribute__((aligned(16))) half_t vs[BM * C::LD];
   __shared__ float back[BM];  // what undoes a row's power of two
   const LoraProblem& p = g.p[blockIdx.z];
   const int first = blockIdx.y * g.columns;
   if (first >= p.n) return;
-  if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile(g, blockIdx.x, tile, masks))) return;
+  if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile<kLoraThreads>(g, blockIdx.x, tile))) return;
   const int end = first + g.columns < p.n ? first + g.columns : p.n;
   const bool wide = wide_columns(p);
   if (tile.slot < 0) {
@@ -442,87 +449,199 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
   }
 }
 
-// ------------------------------------------------------------------- fused
-// Few rows, a small A: both products in one launch.  Every workgroup forms
-// its tile's v itself (the other workgroups of the tile read the same A from
-// L2, on the same XCD where the rows are a multiple of 8), its eight waves
-// taking turns at 64 values of k, then goes on to its columns, whose first
-// loads it has issued before.
-constexpr int kFusedThreads = 512;
-template <int RT>
-__global__ __launch_bounds__(kFusedThreads) void lora_fused_kernel(LoraArgs g) {
-  constexpr int RC = (RT + 1) / 2;
-  constexpr int WAVES = kFusedThreads / 64;
-  using C = Columns<16, RC>;
-  __shared__ TileRows<16> tile;
-  __shared__ uint64_t masks[kLoraDirectRows / 64];
-  __shared__ f4 part[WAVES][RT][64];
-  __shared__ __attribute__((aligned(16))) half_t vs[16 * C::LD];
-  __shared__ float back[16];
+// ---------------------------------------------------------------- few rows
+// Few rows, a small A of rank up to 64: both products in one launch, as dot
+// products of up to kFewRows rows with lanes along memory: a load of 16
+// bytes a lane covers 1 KB of one row of A (or of neighbouring rows of B),
+// where the matrix cores' operand layout touches 16 rows with neighbouring
+// lanes and L1 gives a third of the rate (15 against 44 bytes a clock and CU).
+// Every workgroup forms its tile's v itself (the others of the tile read the
+// same A from L2), then goes on to its columns, whose first loads it has
+// issued before.
+constexpr int kFewThreads = 512;
+constexpr int kFewWaves = kFewThreads / 64;
+constexpr int kFewRows = 4;
+
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float lane_add(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false);
+  return v + __builtin_bit_cast(float, o);
+}
+// The sum over the wave, in its last lane: within the rows of 16, then across
+// them (lanes of rows that receive nothing add zero).
+__device__ __forceinline__ float sum_to_last(float v) {
+  v = lane_add<0xB1>(v);
+  v = lane_add<0x4E>(v);
+  v = lane_add<0x141>(v);
+  v = lane_add<0x140>(v);
+  v = lane_add<0x142, 0xA>(v);
+  return lane_add<0x143, 0xC>(v);
+}
+
+// v of NR rows by dot products: wave w forms rank / 8 of the ranks (at most U).
+template <int U, int NR>
+__device__ __forceinline__ void few_rows_shrink(const LoraArgs& g, const LoraProblem& p, const TileRows<kFewRows>& tile,
+                                                float (*v)[64]) {
+  constexpr int UK = NR > 1 ? (U <= 2 ? 2 : 1) : U <= 2 ? 4 : U == 4 ? 2 : 1;  // steps of 512 values of k in flight
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int ranks = p.rank >> 3;
+  auto ap = to_global(p.a) + ((size_t)tile.slot * p.rank + wave * ranks) * p.k;
+  gptr<uint16_t> xp[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+    xp[r] = to_global(p.x) + (size_t)lora_x_row(g, p, tile.rows[r < tile.count ? r : tile.count - 1]) * p.k;
+  float acc[U][NR];
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int r = 0; r < NR; ++r) acc[i][r] = 0.0f;
+  for (int k0 = lane * 8; k0 < p.k + lane * 8; k0 += 512 * UK) {
+    u32x4 a[UK][U], x[UK][NR];
+#pragma unroll
+    for (int u = 0; u < UK; ++u) {
+      const int k = k0 + u * 512;
+      const bool in = k < p.k;
+      const int at = in ? k : 0;
+#pragma unroll
+      for (int i = 0; i < U; ++i) a[u][i] = *(gptr<u32x4>)(ap + (size_t)(i < ranks ? i : 0) * p.k + at);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        x[u][r] = *(gptr<u32x4>)(xp[r] + at);
+        if (!in) x[u][r] = u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UK; ++u)
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][r] = dot2(a[u][i][j], x[u][r][j], acc[i][r]);
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float s = sum_to_last(acc[i][r]);
+      if (lane == 63 && i < ranks) v[r][wave * ranks + i] = s;
+    }
+}
+
+// A wave's columns by dot products: U neighbouring lanes (rank / 8 of them at
+// work, a power of two in all) share a column, a load covers 64 / U columns,
+// four loads are one turn.  Lane u of
+// the U adds to base and stores the rows u, u + U, ... (RH of them; rows and
+// columns past the end are loaded again from the last one and not stored).
+template <int U, int NR>
+struct FewColumns {
+  static constexpr int kPerLoad = 64 / U;
+  static constexpr int RH = (NR + U - 1) / U;
+  const LoraProblem& p;
+  gptr<uint16_t> bp;
+  size_t row[RH];
+  bool live[RH];
+  int unit, col;
+  h8 b[4];
+  float o[4][RH];
+
+  __device__ __forceinline__ FewColumns(const LoraProblem& p_, const TileRows<kFewRows>& tile) : p(p_) {
+    unit = threadIdx.x & (U - 1);
+    col = (threadIdx.x & 63) / U;
+    const int units = p.rank >> 3;
+    bp = to_global(p.b) + (size_t)tile.slot * p.n * p.rank + (unit < units ? unit : units - 1) * 8;
+#pragma unroll
+    for (int h = 0; h < RH; ++h) {
+      const int r = h * U + unit;
+      live[h] = r < tile.count;
+      row[h] = (size_t)tile.rows[live[h] ? r : tile.count - 1] * p.n;
+    }
+  }
+
+  __device__ __forceinline__ void load(int n0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + j * kPerLoad + col < p.n ? n0 + j * kPerLoad + col : p.n - 1;
+      b[j] = *(gptr<h8>)(bp + (size_t)n * p.rank);
+#pragma unroll
+      for (int h = 0; h < RH; ++h) o[j][h] = 0.0f;
+    }
+    if (p.base == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + j * kPerLoad + col < p.n ? n0 + j * kPerLoad + col : p.n - 1;
+#pragma unroll
+      for (int h = 0; h < RH; ++h) o[j][h] = to_global(p.base)[row[h] + n];
+    }
+  }
+
+  __device__ __forceinline__ void finish(int n0, int end, const float (&v)[NR][8], float scale) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + j * kPerLoad + col;
+      float d[RH * U];
+#pragma unroll
+      for (int r = 0; r < RH * U; ++r) {
+        d[r] = 0.0f;
+        if (r >= NR) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[r] = fmaf((float)b[j][i], v[r][i], d[r]);
+        if (U > 1) d[r] = lane_add<0xB1>(d[r]);
+        if (U > 2) d[r] = lane_add<0x4E>(d[r]);
+        if (U > 4) d[r] = lane_add<0x141>(d[r]);
+      }
+#pragma unroll
+      for (int h = 0; h < RH; ++h) {
+        float mine = d[h * U];
+#pragma unroll
+        for (int u = 1; u < U; ++u) mine = unit == u ? d[h * U + u] : mine;
+        if (live[h] && n < end) to_global_mut(p.y)[row[h] + n] = fmaf(scale, mine, o[j][h]);
+      }
+    }
+  }
+};
+
+template <int U, int NR>
+__device__ __forceinline__ void few_rows(const LoraArgs& g, const LoraProblem& p, const TileRows<kFewRows>& tile,
+                                         int first, int end, float (*vs)[64]) {
+  using C = FewColumns<U, NR>;
+  const int wave = threadIdx.x >> 6;
+  const float scale = g.scales ? g.scales[tile.slot / g.experts] : 1.0f;
+  C cols(p, tile);
+  int n0 = first + wave * 4 * C::kPerLoad;
+  cols.load(n0);
+  few_rows_shrink<U, NR>(g, p, tile, vs);
+  __syncthreads();
+  float v[NR][8];
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[r][i] = cols.unit * 8 < p.rank ? vs[r][cols.unit * 8 + i] : 0.0f;
+  for (;;) {
+    cols.finish(n0, end, v, scale);
+    n0 += kFewWaves * 4 * C::kPerLoad;
+    if (n0 >= end) break;
+    cols.load(n0);
+  }
+}
+
+template <int U>
+__global__ __launch_bounds__(kFewThreads) void lora_few_kernel(LoraArgs g) {
+  __shared__ TileRows<kFewRows> tile;
+  __shared__ float vs[kFewRows][64];
   const LoraProblem& p = g.p[blockIdx.z];
   const int first = blockIdx.y * g.columns;
   if (first >= p.n) return;
-  if (!find_tile(g, blockIdx.x, tile, masks)) return;
+  if (!find_tile<kFewThreads>(g, blockIdx.x, tile)) return;
   const int end = first + g.columns < p.n ? first + g.columns : p.n;
-  const bool wide = wide_columns(p);
   if (tile.slot < 0) {
-    plain_rows(p, tile, first, end, wide);
+    plain_rows(p, tile, first, end, wide_columns(p));
     return;
   }
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int li = lane & 15;
-  const int q = lane >> 4;
-  const int row = tile.rows[li < tile.count ? li : tile.count - 1];
-  auto xp = to_global(p.x) + (size_t)lora_x_row(g, p, row) * p.k + q * 16;
-  gptr<uint16_t> ap[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int r = i * 16 + li < p.rank ? i * 16 + li : p.rank - 1;
-    ap[i] = to_global(p.a) + ((size_t)tile.slot * p.rank + r) * p.k + q * 16;
-  }
-  f4 acc[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-#pragma unroll 4
-  for (int k = wave * 64; k < p.k; k += WAVES * 64) {
-    const h8 x0 = *(gptr<h8>)(xp + k), x1 = *(gptr<h8>)(xp + k + 8);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const h8 a0 = *(gptr<h8>)(ap[i] + k), a1 = *(gptr<h8>)(ap[i] + k + 8);
-      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, x0, acc[i], 0, 0, 0);
-      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, x1, acc[i], 0, 0, 0);
-    }
-  }
-  const int step = wave * 64 + li * 4;
-  C cols;
-  cols.load(p, tile, first + step, end, wide);
-#pragma unroll
-  for (int i = 0; i < RT; ++i) part[wave][i][lane] = acc[i];
-  __syncthreads();
-  // thread (m, u0 of 32): the 8 ranks of unit u0 are two quads of a block's 16
-  constexpr int TPR = kFusedThreads / 16;
-  const int m = threadIdx.x / TPR;
-  const int u0 = threadIdx.x % TPR;
-  f4 f[1][2];
-  f[0][0] = f[0][1] = f4{0, 0, 0, 0};
-  if (u0 * 8 < p.rank) {
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      f[0][0] += part[w][u0 >> 1][(u0 & 1) * 32 + m];
-      f[0][1] += part[w][u0 >> 1][(u0 & 1) * 32 + 16 + m];
-    }
-  }
-  split_row<RC, C::LD, TPR, 1>(f, m, u0, vs, back);
-  __syncthreads();
-
-  const float scale = g.scales ? g.scales[tile.slot / g.experts] : 1.0f;
-  for (int n = first;;) {
-    cols.finish(p, tile, n + step, end, wide, vs, back, scale);
-    n += kFusedThreads;
-    if (n >= end) break;
-    cols.load(p, tile, n + step, end, wide);
-  }
+  if (tile.count == 1) few_rows<U, 1>(g, p, tile, first, end, vs);
+  else if (tile.count == 2) few_rows<U, 2>(g, p, tile, first, end, vs);
+  else few_rows<U, kFewRows>(g, p, tile, first, end, vs);
 }
 
 // ------------------------------------------------------------------- route
@@ -693,13 +812,21 @@ static long lora_tiles(int rows, int tile_rows, int slots) {
 // Tile height, splits of k, columns of a workgroup, chunks of the route and
 // the places of everything in the workspace; its size.
 size_t lora_layout(LoraArgs& g) {
-  g.direct = g.rows <= kLoraDirectRows;
   int rank = 0;
-  for (int i = 0; i < g.count; ++i) rank = g.p[i].rank > rank ? g.p[i].rank : rank;
-  g.tile_rows = g.direct || rank > 128 || g.rows < 24 * g.slots || g.rows < 1024 ? 16 : 64;
+  long a_bytes = 0;  // the largest A of a slot
+  for (int i = 0; i < g.count; ++i) {
+    rank = g.p[i].rank > rank ? g.p[i].rank : rank;
+    const long a = 2L * g.p[i].rank * g.p[i].k;
+    a_bytes = a > a_bytes ? a : a_bytes;
+  }
+  static const int lim = getenv("QMM_LORA_FEW") ? atoi(getenv("QMM_LORA_FEW")) : 512;
+  const bool few = g.rows <= lim && rank <= 64 && rank * g.rows <= 8192 && a_bytes <= 640 * 1024;
+  g.way = few ? kLoraFew : g.rows <= kLoraDirectRows ? kLoraDirect : kLoraRouted;
+  const bool direct = g.way != kLoraRouted;
+  g.tile_rows = direct || rank > 128 || g.rows < 24 * g.slots || g.rows < 1024 ? 16 : 64;
   size_t ints = 0;
   g.tiles = g.rows;
-  if (!g.direct) {
+  if (!direct) {
     const int buckets = g.slots + 2;
     g.chunks = kLoraCountWords / buckets;
     g.chunks = g.chunks < 1 ? 1 : g.chunks > 64 ? 64 : g.chunks;
@@ -718,8 +845,7 @@ size_t lora_layout(LoraArgs& g) {
     int splits = (p.k + 511) / 512;
     if (g.tile_rows == 64) {
       const long wgs = (long)(g.rows + 63) / 64 * ((p.rank + 63) / 64);
-      static const long tgt = getenv("QMM_LORA_S") ? atol(getenv("QMM_LORA_S")) : 512;
-      const long want = (tgt + wgs - 1) / wgs;
+      const long want = (256 + wgs - 1) / wgs;
       splits = splits < want ? splits : (int)want;
     }
     splits = splits > 8 ? 8 : splits;
@@ -766,37 +892,35 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
   else if constexpr (BM == 16) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 8>), eg, block, 0, st, g);
 }
 
-// One launch where every problem's A is small enough to be read again by
-// each workgroup of a tile.
-static bool lora_fused(const LoraArgs& g) {
-  static const long most = getenv("QMM_LORA_FUSED") ? atol(getenv("QMM_LORA_FUSED")) : 192;
-  for (int i = 0; i < g.count; ++i)
-    if (g.p[i].rank > 64 || (long)g.p[i].rank_pad * g.p[i].k * 2 > most * 1024) return false;
-  return true;
-}
-
-static void launch_lora_fused(LoraArgs g, hipStream_t st) {
-  int rank = 1, n = 1;
+static void launch_lora_few(LoraArgs g, hipStream_t st) {
+  int n = 1, rank = 8;
   long columns = 0;  // of all problems
   for (int i = 0; i < g.count; ++i) {
-    rank = g.p[i].rank > rank ? g.p[i].rank : rank;
     n = g.p[i].n > n ? g.p[i].n : n;
+    rank = g.p[i].rank > rank ? g.p[i].rank : rank;
     columns += g.p[i].n;
   }
-  static const long target = getenv("QMM_LORA_WGS") ? atol(getenv("QMM_LORA_WGS")) : 512;
-  long per = (columns * g.rows + target - 1) / target;
-  per = (per + 511) / 512 * 512;
-  g.columns = (int)(per < 512 ? 512 : per > 4096 ? 4096 : per);
-  const dim3 grid(g.rows, (n + g.columns - 1) / g.columns, g.count), block(kFusedThreads);
-  if (rank <= 16) hipLaunchKernelGGL(lora_fused_kernel<1>, grid, block, 0, st, g);
-  else if (rank <= 32) hipLaunchKernelGGL(lora_fused_kernel<2>, grid, block, 0, st, g);
-  else hipLaunchKernelGGL(lora_fused_kernel<4>, grid, block, 0, st, g);
+  const int units = rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 ? 4 : 8;
+  const int turn = kFewWaves * 4 * 64 / units;  // columns of a workgroup's turn
+  long per = (columns * g.rows + 255) / 256;    // one workgroup a CU
+  per = (per + turn - 1) / turn * turn;
+  g.columns = (int)(per < 4096 ? per : 4096);
+  const dim3 grid(g.rows, (n + g.columns - 1) / g.columns, g.count), block(kFewThreads);
+  switch (units) {
+    case 1: hipLaunchKernelGGL(lora_few_kernel<1>, grid, block, 0, st, g); break;
+    case 2: hipLaunchKernelGGL(lora_few_kernel<2>, grid, block, 0, st, g); break;
+    case 4: hipLaunchKernelGGL(lora_few_kernel<4>, grid, block, 0, st, g); break;
+    default: hipLaunchKernelGGL(lora_few_kernel<8>, grid, block, 0, st, g); break;
+  }
 }
 
 hipError_t launch_lora(const LoraArgs& g, hipStream_t st) {
-  if (g.direct) {
-    if (lora_fused(g)) launch_lora_fused(g, st);
-    else launch_lora_products<false, 16>(g, st);
+  if (g.way == kLoraFew) {
+    launch_lora_few(g, st);
+    return hipGetLastError();
+  }
+  if (g.way == kLoraDirect) {
+    launch_lora_products<false, 16>(g, st);
     return hipGetLastError();
   }
   if (g.chunks > 1) hipLaunchKernelGGL(lora_count_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);

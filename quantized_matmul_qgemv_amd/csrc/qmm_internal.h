@@ -190,7 +190,9 @@ hipError_t launch_moe_topk(const TopkArgs& a, hipStream_t st);
 constexpr int kLoraMaxProblems = 8;
 constexpr int kLoraMaxSlots = 4096;     // adapters x experts: one LDS counter each
 constexpr int kLoraMaxRank = 256;
-constexpr int kLoraDirectRows = 256;    // rows up to which every workgroup finds its tile itself
+constexpr int kLoraFewRows = 512;       // rows up to which a workgroup of 512 finds its tile itself
+constexpr int kLoraDirectRows = 256;    // and one of 256
+enum { kLoraFew, kLoraDirect, kLoraRouted };
 constexpr int kLoraPlanHeader = 8;      // words before the sorted rows
 constexpr int kLoraCountWords = 65536;  // chunks x buckets at most
 constexpr int kLoraChunkMin = 1024;     // rows a chunk at least
@@ -214,7 +216,7 @@ struct LoraArgs {
   int32_t* plan;               // the workspace, as words: header, sorted rows, tiles, counts
   size_t plan_tiles, plan_counts;
   int32_t count, rows, top_k, adapters, experts, slots;
-  int32_t direct, tile_rows, columns, chunk, chunks;
+  int32_t way, tile_rows, columns, chunk, chunks;
   int64_t tiles;  // most tiles that the rows can form
 };
 size_t lora_layout(LoraArgs& g);
