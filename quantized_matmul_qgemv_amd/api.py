@@ -291,18 +291,40 @@ def moe_combine(y_pairs, weights, y=None, stream=None):
 
 
 _SCORES = {"softmax": _lib.QMM_SCORE_SOFTMAX, "sigmoid": _lib.QMM_SCORE_SIGMOID}
+_I = (torch.int32,)
 
 
-def _same_device(first: torch.Tensor, *others) -> None:
-    """Every tensor on one device, and that device current: the launch goes
-    there, whatever memory the pointers name."""
-    index = first.device.index
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The device of t, which has to be the current one: a launch goes there,
+    whatever memory its pointers name."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a device tensor")
     if index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{index}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    for t in others:
-        if t is not None and t.device.index != index:
-            raise ValueError(f"the tensors are on cuda:{index} and {t.device}")
+        raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    return index
+
+
+def _ptr(t, name: str, dtypes, index: int):
+    """_dev for a tensor that has to be on device `index` (None -> NULL)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() < 0:
+        _dev(t, name, dtypes)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the others on cuda:{index}")
+    return t.data_ptr()
+
+
+def _stream_on(stream, index: int) -> int:
+    """The given stream, which has to be one of device `index`, or its current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
+    return stream.cuda_stream
 
 
 def moe_topk(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1,
@@ -319,20 +341,22 @@ def moe_topk(logits, top_k: int, bias=None, score: str = "softmax", groups: int 
     if score not in _SCORES:
         raise ValueError(f"score must be one of {tuple(_SCORES)}, not {score!r}")
     t, e = logits.shape
+    want = (t, top_k)
     if bias is not None and bias.shape != (e,):
         raise ValueError(f"bias must be [{e}], not {tuple(bias.shape)}")
     if expert_ids is None:
         expert_ids = torch.empty((t, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+    elif expert_ids.shape != want:
+        raise ValueError(f"expert_ids must be [{t}, {top_k}], not {tuple(expert_ids.shape)}")
     if weights is None:
         weights = torch.empty((t, max(top_k, 0)), dtype=torch.float32, device=logits.device)
-    for out, name in ((expert_ids, "expert_ids"), (weights, "weights")):
-        if out.shape != (t, top_k):
-            raise ValueError(f"{name} must be [{t}, {top_k}], not {tuple(out.shape)}")
-    lp, ip, wp = _dev(logits, "logits", _Y), _dev(expert_ids, "expert_ids", (torch.int32,)), _dev(weights, "weights", _Y)
-    bp = None if bias is None else _dev(bias, "bias", _Y)
-    _same_device(logits, bias, expert_ids, weights)
-    check(lib().qmm_moe_topk(lp, bp, ip, wp, t, e, top_k, _SCORES[score], groups, group_keep, group_top,
-                             int(bool(renormalize)), scale, _stream(stream)))
+    elif weights.shape != want:
+        raise ValueError(f"weights must be [{t}, {top_k}], not {tuple(weights.shape)}")
+    d = _device_of(logits, "logits")
+    check(lib().qmm_moe_topk(_ptr(logits, "logits", _Y, d), _ptr(bias, "bias", _Y, d),
+                             _ptr(expert_ids, "expert_ids", _I, d), _ptr(weights, "weights", _Y, d), t, e,
+                             top_k, _SCORES[score], groups, group_keep, group_top, 1 if renormalize else 0, scale,
+                             _stream_on(stream, d)))
     return expert_ids, weights
 
 
@@ -347,29 +371,10 @@ def _lora_rows(problems, adapter_ids, expert_ids):
         if expert_ids.dim() != 2 or expert_ids.shape[0] != t:
             raise ValueError(f"expert_ids must be [{t}, top_k], not {tuple(expert_ids.shape)}")
         top_k = expert_ids.shape[1]
-    a = problems[0][1]
-    return t, top_k, a.numel() // (a.shape[-1] * a.shape[-2])
-
-
-def _lora_array(problems, t, top_k, slots, x_row_per_pair):
-    """The problems as the C ABI's array, their shapes checked against each other."""
-    arr = (LoraProblem * len(problems))()
-    for i, (x, a, b, base, y) in enumerate(problems):
-        rank, k, n = a.shape[-2], a.shape[-1], b.shape[-2]
-        want = (t * top_k if x_row_per_pair else t, k)
-        if x.shape != want:
-            raise ValueError(f"problem {i}: x must be {list(want)}, not {tuple(x.shape)}")
-        if a.numel() != slots * rank * k or b.shape[-1] != rank or b.numel() != slots * n * rank:
-            raise ValueError(f"problem {i}: a {tuple(a.shape)} and b {tuple(b.shape)} must be [{slots}, rank, k] "
-                             f"and [{slots}, n, rank]")
-        for o, name in ((base, "base"), (y, "y")):
-            if o is not None and o.shape != (t * top_k, n):
-                raise ValueError(f"problem {i}: {name} must be [{t * top_k}, {n}], not {tuple(o.shape)}")
-        arr[i] = LoraProblem(_dev(x, "x", _X), _dev(a, "a", _X), _dev(b, "b", _X),
-                             None if base is None else _dev(base, "base", _Y), _dev(y, "y", _Y), n, k, rank,
-                             int(bool(x_row_per_pair)))
-        _same_device(x, a, b, base, y)
-    return arr
+    shape = problems[0][1].shape
+    if len(shape) < 3:
+        raise ValueError(f"problem 0: a must be [adapters, rank, k], not {tuple(shape)}")
+    return t, top_k, shape[0] if len(shape) == 3 else shape[0] * shape[1]
 
 
 def lora_workspace(problems, adapter_ids, expert_ids=None):
@@ -387,7 +392,7 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
                  workspace=None, stream=None):
     """y = base + scales[id] * B_id (A_id x) for the projections of one input
     (q, k and v; gate and up) in the same launches, via qmm_lora: a list of
-    (x, a, b, base, y) with base None or y itself to add in place.
+    (x, a, b, base, y) with base None, or y itself to add in place.
     adapter_ids int32 [T], -1 for no adapter; a [adapters, rank, k] and
     b [adapters, n, rank] fp16.  With expert_ids [T, top_k] the rows are the
     pairs of a routed layer and each adapter has weights for every expert
@@ -395,7 +400,7 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
     list of y."""
     t, top_k, slots = _lora_rows(problems, adapter_ids, expert_ids)
     a = problems[0][1]
-    experts = 0
+    experts, adapters = 0, slots
     if expert_ids is not None:
         if a.dim() == 4:
             experts = a.shape[1]
@@ -403,24 +408,40 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
             experts = slots // scales.numel()
         else:
             raise ValueError("a must be [adapters, experts, rank, k] (or scales [adapters] be given)")
-    adapters = slots // max(1, experts)
-    if adapters * max(1, experts) != slots:
-        raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
+        adapters = slots // max(1, experts)
+        if adapters * experts != slots:
+            raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
     if scales is not None and scales.shape != (adapters,):
         raise ValueError(f"scales must be [{adapters}], not {tuple(scales.shape)}")
-    problems = [p if p[4] is not None else (*p[:4], torch.empty(
-        (t * top_k, p[2].shape[-2]), dtype=torch.float32, device=p[0].device)) for p in problems]
-    arr = _lora_array(problems, t, top_k, slots, x_row_per_pair)
-    ip = _dev(adapter_ids, "adapter_ids", (torch.int32,))
-    ep = None if expert_ids is None else _dev(expert_ids, "expert_ids", (torch.int32,))
-    sp = None if scales is None else _dev(scales, "scales", _Y)
+    rows, per_pair = t * top_k, 1 if x_row_per_pair else 0
+    x_rows = rows if per_pair else t
+    d, checked, out = None, [], []
+    for i, (x, a, b, base, y) in enumerate(problems):
+        rank, k = a.shape[-2:]
+        n = b.shape[-2]
+        if x.shape != (x_rows, k):
+            raise ValueError(f"problem {i}: x must be [{x_rows}, {k}], not {tuple(x.shape)}")
+        if a.numel() != slots * rank * k or b.shape[-1] != rank or b.numel() != slots * n * rank:
+            raise ValueError(f"problem {i}: a {tuple(a.shape)} and b {tuple(b.shape)} must be [{slots}, rank, k] "
+                             f"and [{slots}, n, rank]")
+        if base is not None and base.shape != (rows, n):
+            raise ValueError(f"problem {i}: base must be [{rows}, {n}], not {tuple(base.shape)}")
+        if y is None:
+            y = torch.empty((rows, n), dtype=torch.float32, device=x.device)
+        elif y.shape != (rows, n):
+            raise ValueError(f"problem {i}: y must be [{rows}, {n}], not {tuple(y.shape)}")
+        if d is None:
+            d = _device_of(x, "x")
+        checked.append(LoraProblem(_ptr(x, "x", _X, d), _ptr(a, "a", _X, d), _ptr(b, "b", _X, d),
+                                   _ptr(base, "base", _Y, d), _ptr(y, "y", _Y, d), n, k, rank, per_pair))
+        out.append(y)
     if workspace is None:
         workspace = lora_workspace(problems, adapter_ids, expert_ids)
-    wp = _dev(workspace, "workspace", (torch.uint8,))
-    _same_device(problems[0][0], adapter_ids, expert_ids, scales, workspace)
-    check(lib().qmm_lora(arr, len(problems), ip, ep, sp, t, top_k, adapters, experts, wp, workspace.numel(),
-                         _stream(stream)))
-    return [p[4] for p in problems]
+    check(lib().qmm_lora((LoraProblem * len(checked))(*checked), len(checked),
+                         _ptr(adapter_ids, "adapter_ids", _I, d), _ptr(expert_ids, "expert_ids", _I, d),
+                         _ptr(scales, "scales", _Y, d), t, top_k, adapters, experts,
+                         _ptr(workspace, "workspace", (torch.uint8,), d), workspace.numel(), _stream_on(stream, d)))
+    return out
 
 
 def lora(x, a, b, adapter_ids, scales=None, base=None, y=None, expert_ids=None,

@@ -21,8 +21,6 @@
 //
 // Every row is computed on its own (neither its tile nor its place in it
 // enters the sums), so results do not depend on scheduling.
-#include <stdlib.h>
-
 #include "qmm_device.h"
 #include "qmm_internal.h"
 
@@ -626,14 +624,14 @@ __device__ __forceinline__ void few_rows(const LoraArgs& g, const LoraProblem& p
   }
 }
 
-template <int U>
+template <bool ROUTED, int U>
 __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(LoraArgs g) {
   __shared__ TileRows<kFewRows> tile;
   __shared__ float vs[kFewRows][64];
   const LoraProblem& p = g.p[blockIdx.z];
   const int first = blockIdx.y * g.columns;
   if (first >= p.n) return;
-  if (!find_tile<kFewThreads>(g, blockIdx.x, tile)) return;
+  if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile<kFewThreads>(g, blockIdx.x, tile))) return;
   const int end = first + g.columns < p.n ? first + g.columns : p.n;
   if (tile.slot < 0) {
     plain_rows(p, tile, first, end, wide_columns(p));
@@ -651,6 +649,7 @@ __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(LoraArgs g) {
 // before it.  Buckets slots and slots + 1 hold the rows without adapter and
 // those with bad ids.
 constexpr int kRouteThreads = 1024;
+static_assert(kFewRows <= 16, "the smallest tile");
 static_assert(kLoraOneChunk == 4 * kRouteThreads, "one chunk's rows are four of each thread");
 constexpr int kLoraBuckets = kLoraMaxSlots + 2;
 
@@ -809,8 +808,21 @@ static long lora_tiles(int rows, int tile_rows, int slots) {
   return most < rows ? most : rows;
 }
 
-// Tile height, splits of k, columns of a workgroup, chunks of the route and
-// the places of everything in the workspace; its size.
+// The way a call takes, its tile height, splits of k, chunks of the route and
+// the places of everything in the workspace; its size.  By total time of the
+// launches of a call (k and n as given, microseconds):
+//   one launch of dot products (few) against two on the matrix cores, 64
+//     rows: 7.0 / 13.6 (rank 16, 2560, 4096), 9.9 / 16.2 (rank 16, 9728,
+//     4096), 14.7 / 19.2 (rank 32, 9728: A of 608 KB), 34.9 / 32.0 (rank 64,
+//     9728: 1.2 MB); 256 rows of rank 64 (2560, 4096): 35.1 / 29.8, of rank
+//     32: 20.2 / 22.3; 512 rows of rank 16 against sorted ones (1024, 1024):
+//     9.7 / 13.9.  Hence A up to 640 KB and rows x rank up to 8192.
+//   sorted rows, tiles of 4 for dot products against tiles of 16 (768,
+//     2048): rank 8 with 8 rows a slot 32.4 / 37.9, rank 16 with 4 24.7 / 34.0
+//     and with 8 41.1 / 39.3, rank 32 with 2 27.3 / 32.3 and with 4 40.4 /
+//     37.8, rank 64 with 2 47.9 / 47.9.  Hence rows x rank up to 96 a slot.
+//   sorted rows, tiles of 64 where they are filled and there are enough of
+//     them to fill the chip; [hi | lo] of a rank over 128 outgrows LDS there.
 size_t lora_layout(LoraArgs& g) {
   int rank = 0;
   long a_bytes = 0;  // the largest A of a slot
@@ -819,11 +831,14 @@ size_t lora_layout(LoraArgs& g) {
     const long a = 2L * g.p[i].rank * g.p[i].k;
     a_bytes = a > a_bytes ? a : a_bytes;
   }
-  static const int lim = getenv("QMM_LORA_FEW") ? atoi(getenv("QMM_LORA_FEW")) : 512;
-  const bool few = g.rows <= lim && rank <= 64 && rank * g.rows <= 8192 && a_bytes <= 640 * 1024;
-  g.way = few ? kLoraFew : g.rows <= kLoraDirectRows ? kLoraDirect : kLoraRouted;
+  const bool small = rank <= 64 && a_bytes <= 640 * 1024;
+  g.way = small && g.rows <= kLoraFewRows && rank * g.rows <= 8192 ? kLoraFew
+          : g.rows <= kLoraDirectRows                              ? kLoraDirect
+                                                                   : kLoraRouted;
   const bool direct = g.way != kLoraRouted;
-  g.tile_rows = direct || rank > 128 || g.rows < 24 * g.slots || g.rows < 1024 ? 16 : 64;
+  g.tile_rows = !direct && small && (long)g.rows * rank <= 96L * g.slots            ? kFewRows
+                : direct || rank > 128 || g.rows < 24 * g.slots || g.rows < 1024 ? 16
+                                                                                  : 64;
   size_t ints = 0;
   g.tiles = g.rows;
   if (!direct) {
@@ -892,6 +907,7 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
   else if constexpr (BM == 16) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 8>), eg, block, 0, st, g);
 }
 
+template <bool ROUTED>
 static void launch_lora_few(LoraArgs g, hipStream_t st) {
   int n = 1, rank = 8;
   long columns = 0;  // of all problems
@@ -905,18 +921,18 @@ static void launch_lora_few(LoraArgs g, hipStream_t st) {
   long per = (columns * g.rows + 255) / 256;    // one workgroup a CU
   per = (per + turn - 1) / turn * turn;
   g.columns = (int)(per < 4096 ? per : 4096);
-  const dim3 grid(g.rows, (n + g.columns - 1) / g.columns, g.count), block(kFewThreads);
+  const dim3 grid((unsigned)(ROUTED ? up(g.tiles, kXcds) : g.rows), (n + g.columns - 1) / g.columns, g.count), block(kFewThreads);
   switch (units) {
-    case 1: hipLaunchKernelGGL(lora_few_kernel<1>, grid, block, 0, st, g); break;
-    case 2: hipLaunchKernelGGL(lora_few_kernel<2>, grid, block, 0, st, g); break;
-    case 4: hipLaunchKernelGGL(lora_few_kernel<4>, grid, block, 0, st, g); break;
-    default: hipLaunchKernelGGL(lora_few_kernel<8>, grid, block, 0, st, g); break;
+    case 1: hipLaunchKernelGGL((lora_few_kernel<ROUTED, 1>), grid, block, 0, st, g); break;
+    case 2: hipLaunchKernelGGL((lora_few_kernel<ROUTED, 2>), grid, block, 0, st, g); break;
+    case 4: hipLaunchKernelGGL((lora_few_kernel<ROUTED, 4>), grid, block, 0, st, g); break;
+    default: hipLaunchKernelGGL((lora_few_kernel<ROUTED, 8>), grid, block, 0, st, g); break;
   }
 }
 
 hipError_t launch_lora(const LoraArgs& g, hipStream_t st) {
   if (g.way == kLoraFew) {
-    launch_lora_few(g, st);
+    launch_lora_few<false>(g, st);
     return hipGetLastError();
   }
   if (g.way == kLoraDirect) {
@@ -925,7 +941,8 @@ hipError_t launch_lora(const LoraArgs& g, hipStream_t st) {
   }
   if (g.chunks > 1) hipLaunchKernelGGL(lora_count_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);
   hipLaunchKernelGGL(lora_place_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);
-  if (g.tile_rows == 64) launch_lora_products<true, 64>(g, st);
+  if (g.tile_rows == kFewRows) launch_lora_few<true>(g, st);
+  else if (g.tile_rows == 64) launch_lora_products<true, 64>(g, st);
   else launch_lora_products<true, 16>(g, st);
   return hipGetLastError();
 }
