@@ -368,7 +368,7 @@ int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, fl
  * The up to 8 problems of one call (q, k and v; gate and up) share the ids and
  * run in the same launches; their y must not overlap.  Adapters of smaller
  * rank are padded with zeros to the problem's rank, a multiple of 8 up to
- * 256; k is a multiple of 64, adapters x experts at most 4096, n at most
+ * 256; k is a multiple of 64 up to 2^24, adapters x experts at most 4096, n at most
  * 2097152, t * top_k at most 2^27.  A B x is held in fp32 throughout (products of fp16, A x exact to
  * 2^-23 of the row's largest value); non-finite adapter weights make
  * non-finite outputs.  Results do not depend on scheduling, nor on what the

@@ -327,6 +327,15 @@ def _stream_on(stream, index: int) -> int:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor of the given stream's own memory: what a call allocates itself
+    is not handed to others before that stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def moe_topk(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1,
              group_keep: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
              expert_ids=None, weights=None, stream=None):
@@ -345,11 +354,11 @@ def moe_topk(logits, top_k: int, bias=None, score: str = "softmax", groups: int 
     if bias is not None and bias.shape != (e,):
         raise ValueError(f"bias must be [{e}], not {tuple(bias.shape)}")
     if expert_ids is None:
-        expert_ids = torch.empty((t, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+        expert_ids = _empty((t, max(top_k, 0)), torch.int32, logits.device, stream)
     elif expert_ids.shape != want:
         raise ValueError(f"expert_ids must be [{t}, {top_k}], not {tuple(expert_ids.shape)}")
     if weights is None:
-        weights = torch.empty((t, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+        weights = _empty((t, max(top_k, 0)), torch.float32, logits.device, stream)
     elif weights.shape != want:
         raise ValueError(f"weights must be [{t}, {top_k}], not {tuple(weights.shape)}")
     d = _device_of(logits, "logits")
@@ -377,7 +386,7 @@ def _lora_rows(problems, adapter_ids, expert_ids):
     return t, top_k, shape[0] if len(shape) == 3 else shape[0] * shape[1]
 
 
-def lora_workspace(problems, adapter_ids, expert_ids=None):
+def lora_workspace(problems, adapter_ids, expert_ids=None, stream=None):
     """A workspace for lora and lora_batched calls of these sizes (kept by the
     caller; calls that share one must not overlap in time)."""
     t, top_k, slots = _lora_rows(problems, adapter_ids, expert_ids)
@@ -385,7 +394,7 @@ def lora_workspace(problems, adapter_ids, expert_ids=None):
     for i, (_, a, b, _, _) in enumerate(problems):
         arr[i] = LoraProblem(None, None, None, None, None, b.shape[-2], a.shape[-1], a.shape[-2], 0)
     need = lib().qmm_lora_workspace_size(arr, len(problems), t * top_k, slots)
-    return torch.empty(max(need, 16), dtype=torch.uint8, device=adapter_ids.device)
+    return _empty(max(need, 16), torch.uint8, adapter_ids.device, stream)
 
 
 def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_pair: bool = False,
@@ -427,7 +436,7 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
         if base is not None and base.shape != (rows, n):
             raise ValueError(f"problem {i}: base must be [{rows}, {n}], not {tuple(base.shape)}")
         if y is None:
-            y = torch.empty((rows, n), dtype=torch.float32, device=x.device)
+            y = _empty((rows, n), torch.float32, x.device, stream)
         elif y.shape != (rows, n):
             raise ValueError(f"problem {i}: y must be [{rows}, {n}], not {tuple(y.shape)}")
         if d is None:
@@ -436,7 +445,7 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
                                    _ptr(base, "base", _Y, d), _ptr(y, "y", _Y, d), n, k, rank, per_pair))
         out.append(y)
     if workspace is None:
-        workspace = lora_workspace(problems, adapter_ids, expert_ids)
+        workspace = lora_workspace(problems, adapter_ids, expert_ids, stream)
     check(lib().qmm_lora((LoraProblem * len(checked))(*checked), len(checked),
                          _ptr(adapter_ids, "adapter_ids", _I, d), _ptr(expert_ids, "expert_ids", _I, d),
                          _ptr(scales, "scales", _Y, d), t, top_k, adapters, experts,

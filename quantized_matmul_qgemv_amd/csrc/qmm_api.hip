@@ -82,13 +82,14 @@ int check_plan_size(const char* fn, size_t plan_bytes, int t, int top_k, int e) 
 
 // Rows of one adapter call: tiles of 16, 256 threads each, within 2^32 threads.
 constexpr long kMaxLoraRows = 1 << 27;
+constexpr int kMaxLoraK = 1 << 24;
 constexpr int kMaxLoraN = 1 << 21;  // column blocks of 64 in one grid dimension
 
 int check_lora_sizes(const char* fn, const qmm_lora_problem& q, int i) {
   if (q.n < 1 || q.n > kMaxLoraN)
     return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: n=%d must be in [1, %d]", fn, i, q.n, kMaxLoraN);
-  if (q.k < 64 || q.k % 64 != 0)
-    return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: k=%d must be a positive multiple of 64", fn, i, q.k);
+  if (q.k < 64 || q.k % 64 != 0 || q.k > kMaxLoraK)
+    return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: k=%d must be a positive multiple of 64 up to %d", fn, i, q.k, kMaxLoraK);
   if (q.rank < 8 || q.rank > qmm::kLoraMaxRank || q.rank % 8 != 0)
     return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: rank=%d must be a multiple of 8 in [8, %d]", fn, i,
                 q.rank, qmm::kLoraMaxRank);

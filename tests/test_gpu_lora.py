@@ -40,23 +40,22 @@ def want(x, a, b, ids, scales=None, base=None, expert_ids=None, x_row_per_pair=F
     y = np.zeros((rows, n)) if base is None else base.astype(np.float64)
     y = y.copy()
     worst = HALF * np.abs(y)
-    for p in range(rows):
-        i = int(ids[p // top_k])
-        if i == -1:
-            continue
-        e = None if expert_ids is None else int(expert_ids[p // top_k, p % top_k])
-        if not 0 <= i < adapters or (e is not None and not 0 <= e < a.shape[1]):
-            y[p] = np.nan
-            continue
-        A, B = (a[i], b[i]) if e is None else (a[i, e], b[i, e])
-        A, B = A.astype(np.float64), B.astype(np.float64)
-        xr = x[p if x_row_per_pair else p // top_k].astype(np.float64)
-        s = 1.0 if scales is None else float(scales[i])
-        v = A @ xr
-        ev = 2 * HALF * k * (np.abs(A) @ np.abs(xr)) + 2 * HALF * np.abs(v).max()
-        d = B @ v
-        y[p] += s * d
-        worst[p] += abs(s) * (np.abs(B) @ ev + 2 * HALF * (2 * rank + 2) * (np.abs(B) @ np.abs(v))) + 2 * HALF * np.abs(y[p])
+    adapter = np.repeat(np.asarray(ids, np.int64), top_k)
+    expert = np.zeros(rows, np.int64) if expert_ids is None else expert_ids.reshape(-1).astype(np.int64)
+    experts = 1 if expert_ids is None else a.shape[1]
+    bad = (adapter < -1) | (adapter >= adapters) | ((adapter >= 0) & ((expert < 0) | (expert >= experts)))
+    y[bad] = np.nan
+    slot = np.where(bad | (adapter < 0), -1, adapter * experts + expert)
+    A_, B_ = a.reshape(-1, rank, k), b.reshape(-1, n, rank)
+    for t in np.unique(slot[slot >= 0]):
+        at = np.flatnonzero(slot == t)
+        A, B = A_[t].astype(np.float64), B_[t].astype(np.float64)
+        xr = x[at if x_row_per_pair else at // top_k].astype(np.float64)
+        s = 1.0 if scales is None else float(scales[t // experts])
+        v = xr @ A.T
+        ev = 2 * HALF * k * (np.abs(xr) @ np.abs(A).T) + 2 * HALF * np.abs(v).max(axis=1, keepdims=True)
+        y[at] += s * (v @ B.T)
+        worst[at] += abs(s) * ((ev + 2 * HALF * (2 * rank + 2) * np.abs(v)) @ np.abs(B).T) + 2 * HALF * np.abs(y[at])
     return y, worst + 1e-37
 
 
@@ -139,6 +138,27 @@ SIZES = [
     (4097, 64, 20, 16, 40, "holes"),
     (9000, 128, 24, 8, 4096, "mixed"),
     (6000, 64, 12, 16, 9, "none"),
+    # one launch: ranks that are no power of two, two and three rows a tile, its largest numbers of rows
+    (7, 320, 100, 40, 4, "mixed"),
+    (11, 576, 33, 48, 5, "mixed"),
+    (30, 64, 700, 56, 12, "holes"),
+    (128, 1600, 1025, 64, 60, "mixed"),
+    (512, 192, 130, 16, 9, "bad"),
+    (511, 128, 4100, 8, 3, "runs"),
+    # A too large for one launch
+    (5, 9728, 80, 64, 3, "mixed"),
+    (200, 10240, 40, 40, 2, "holes"),
+    # sorted, tiles of 4
+    (1030, 128, 200, 32, 900, "mixed"),
+    (700, 192, 65, 64, 700, "holes"),
+    (600, 256, 140, 24, 500, "bad"),
+    # sorted, tiles of 64: every rank's kernel, k split and not, several turns of columns
+    (1100, 1088, 301, 128, 2, "holes"),
+    (1500, 704, 600, 64, 3, "runs"),
+    (2100, 2048, 1030, 24, 5, "mixed"),
+    (1024, 64, 256, 32, 1, "same"),
+    (1300, 192, 36, 96, 4, "bad"),
+    (17000, 64, 8200, 8, 3, "runs"),
 ]
 
 
@@ -242,6 +262,19 @@ def test_what_is_not_finite_stays_in_its_row(t):
     assert np.isnan(host(run(x, a, b, ids))[3]).all()
 
 
+def test_magnitudes_of_single_rows():
+    """The same in tiles of one to three rows, subnormal x and A among them."""
+    say("lora magnitudes, few rows")
+    r = np.random.default_rng(91)
+    k, n, rank, t = 576, 50, 16, 6
+    a, b = weights(r, 3, rank, k, n)
+    for xs, as_ in ((1e-6, 1.0), (1.0, 1e-5), (6e4, 6e4), (1e-7, 6e4)):
+        af = np.clip(a.astype(np.float32) * 20 * as_, -65504, 65504).astype(np.float16)
+        x = np.clip(r.standard_normal((t, k)) * xs, -65504, 65504).astype(np.float16)
+        ids = np.array([0, 1, 1, 2, 2, 2], np.int32)
+        check(run(x, af, b, ids), x, af, b, ids, (xs, as_))
+
+
 def test_a_row_does_not_depend_on_the_others():
     say("lora rows alone")
     r = np.random.default_rng(86)
@@ -249,6 +282,7 @@ def test_a_row_does_not_depend_on_the_others():
     a, b = weights(r, 5, rank, k, n)
     x = r.standard_normal((200, k)).astype(np.float16)
     ids = some_ids(r, 200, 5, "holes")
+    ids[:6] = [3, 3, 3, 3, 3, 2]
     whole = host(run(x, a, b, ids))
     for p in (0, 1, 99, 199):
         assert np.array_equal(host(run(x[p:p + 1], a, b, ids[p:p + 1]))[0], whole[p])
@@ -305,6 +339,27 @@ def test_streams_graphs_and_repeats(t):
         assert torch.equal(y, eager)
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own (given, or made by
+    the call), over and over: every result is the one of a call alone."""
+    say("lora two streams")
+    r = np.random.default_rng(92)
+    parts = []
+    for t, k, n, rank in ((3000, 512, 640, 32), (2500, 768, 512, 16)):
+        a, b = weights(r, 4, rank, k, n)
+        parts.append((dev(r.standard_normal((t, k)).astype(np.float16)), dev(a), dev(b), dev(some_ids(r, t, 4, "holes"))))
+    alone = [qmm.lora(*p) for p in parts]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in parts]
+    outs = [[], []]
+    for _ in range(5):
+        for i, (p, st) in enumerate(zip(parts, streams)):
+            outs[i].append(qmm.lora(*p, stream=st))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
+
+
 def test_offsets_past_32_bits():
     """More than 2^31 values of y, and of the adapters' weights."""
     say("lora large offsets")
@@ -341,6 +396,8 @@ def test_offsets_past_32_bits():
 
 def test_no_rows():
     z = lambda *s: torch.zeros(*s, dtype=torch.float16, device="cuda")  # noqa: E731
+    assert qmm.lora(z(0, 64), z(2, 3, 8, 64), z(2, 3, 5, 8), torch.zeros(0, dtype=torch.int32, device="cuda"),
+                    expert_ids=torch.zeros(0, 2, dtype=torch.int32, device="cuda")).shape == (0, 5)
     y = qmm.lora(z(0, 64), z(2, 8, 64), z(2, 5, 8), torch.zeros(0, dtype=torch.int32, device="cuda"))
     assert y.shape == (0, 5)
 

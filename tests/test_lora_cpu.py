@@ -44,6 +44,7 @@ def call(problems=None, count=None, ids=A, experts_ids=None, scales=None, t=4, t
     (dict(n=(1 << 21) + 1), INV, "n=2097153"),
     (dict(k=0), INV, "k=0"),
     (dict(k=96), INV, "k=96"),
+    (dict(k=(1 << 24) + 64), INV, "k=16777280"),
     (dict(rank=0), INV, "rank=0"),
     (dict(rank=12), INV, "rank=12"),
     (dict(rank=264), INV, "rank=264"),
