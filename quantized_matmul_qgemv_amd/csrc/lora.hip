@@ -642,6 +642,85 @@ __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(LoraArgs g) {
   else few_rows<U, kFewRows>(g, p, tile, first, end, vs);
 }
 
+// ---------------------------------------------------------------- fused 16
+// Sorted tiles of 16 rows, a small A: both products in one launch on the
+// matrix cores, as above: the workgroup forms its tile's v (eight waves taking
+// turns at 64 values of k, joined in LDS) and goes on to its columns, whose
+// first loads it has issued before.
+template <int RT>
+__global__ __launch_bounds__(kFewThreads) void lora_fused16_kernel(LoraArgs g) {
+  constexpr int RC = (RT + 1) / 2;
+  using C = Columns<16, RC>;
+  __shared__ TileRows<16> tile;
+  __shared__ f4 part[kFewWaves][RT][64];
+  __shared__ __attribute__((aligned(16))) half_t vs[16 * C::LD];
+  __shared__ float back[16];
+  const LoraProblem& p = g.p[blockIdx.z];
+  const int first = blockIdx.y * g.columns;
+  if (first >= p.n) return;
+  if (!read_tile(g, blockIdx.x, tile)) return;
+  const int end = first + g.columns < p.n ? first + g.columns : p.n;
+  const bool wide = wide_columns(p);
+  if (tile.slot < 0) {
+    plain_rows(p, tile, first, end, wide);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int li = lane & 15;
+  const int q = lane >> 4;
+  const int row = tile.rows[li < tile.count ? li : tile.count - 1];
+  auto xp = to_global(p.x) + (size_t)lora_x_row(g, p, row) * p.k + q * 16;
+  gptr<uint16_t> ap[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = i * 16 + li < p.rank ? i * 16 + li : p.rank - 1;
+    ap[i] = to_global(p.a) + ((size_t)tile.slot * p.rank + r) * p.k + q * 16;
+  }
+  f4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
+#pragma unroll 2
+  for (int k = wave * 64; k < p.k; k += kFewWaves * 64) {
+    const h8 x0 = *(gptr<h8>)(xp + k), x1 = *(gptr<h8>)(xp + k + 8);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const h8 a0 = *(gptr<h8>)(ap[i] + k), a1 = *(gptr<h8>)(ap[i] + k + 8);
+      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, x0, acc[i], 0, 0, 0);
+      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, x1, acc[i], 0, 0, 0);
+    }
+  }
+  const int step = wave * 64 + li * 4;
+  C cols;
+  cols.load(p, tile, first + step, end, wide);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  // thread (m, u0 of 32): the 8 ranks of unit u0 are two quads of a block's 16
+  constexpr int TPR = kFewThreads / 16;
+  const int m = threadIdx.x / TPR;
+  const int u0 = threadIdx.x % TPR;
+  f4 f[1][2];
+  f[0][0] = f[0][1] = f4{0, 0, 0, 0};
+  if (u0 * 8 < p.rank) {
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+      f[0][0] += part[w][u0 >> 1][(u0 & 1) * 32 + m];
+      f[0][1] += part[w][u0 >> 1][(u0 & 1) * 32 + 16 + m];
+    }
+  }
+  split_row<RC, C::LD, TPR, 1>(f, m, u0, vs, back);
+  __syncthreads();
+
+  const float scale = g.scales ? g.scales[tile.slot / g.experts] : 1.0f;
+  for (int n = first;;) {
+    cols.finish(p, tile, n + step, end, wide, vs, back, scale);
+    n += kFewThreads;
+    if (n >= end) break;
+    cols.load(p, tile, n + step, end, wide);
+  }
+}
+
 // ------------------------------------------------------------------- route
 // Rows sorted by slot, and tiles of up to tile_rows rows of one slot, as
 // two launches over chunks of the rows (one if there is one chunk): count
@@ -821,6 +900,10 @@ static long lora_tiles(int rows, int tile_rows, int slots) {
 //     2048): rank 8 with 8 rows a slot 32.4 / 37.9, rank 16 with 4 24.7 / 34.0
 //     and with 8 41.1 / 39.3, rank 32 with 2 27.3 / 32.3 and with 4 40.4 /
 //     37.8, rank 64 with 2 47.9 / 47.9.  Hence rows x rank up to 96 a slot.
+//   sorted rows in tiles of 16, one launch of both products against two (4096
+//     pairs on 512 slots): 28.5 / 33.7 (rank 16, 768, 2048), 53.2 / 57.5
+//     (rank 64, 768, 2048: A of 96 KB), 36.4 / 37.2 (rank 32, 2048, 768),
+//     58.5 / 58.2 (rank 64, 2048, 768: 256 KB).  Hence A up to 128 KB.
 //   sorted rows, tiles of 64 where they are filled and there are enough of
 //     them to fill the chip; [hi | lo] of a rank over 128 outgrows LDS there.
 size_t lora_layout(LoraArgs& g) {
@@ -835,10 +918,11 @@ size_t lora_layout(LoraArgs& g) {
   g.way = small && g.rows <= kLoraFewRows && rank * g.rows <= 8192 ? kLoraFew
           : g.rows <= kLoraDirectRows                              ? kLoraDirect
                                                                    : kLoraRouted;
-  const bool direct = g.way != kLoraRouted;
+  const bool direct = g.way == kLoraFew || g.way == kLoraDirect;
   g.tile_rows = !direct && small && (long)g.rows * rank <= 96L * g.slots            ? kFewRows
                 : direct || rank > 128 || g.rows < 24 * g.slots || g.rows < 1024 ? 16
                                                                                   : 64;
+  if (!direct && g.tile_rows == 16 && rank <= 64 && a_bytes <= 128 * 1024) g.way = kLoraRouted16;
   size_t ints = 0;
   g.tiles = g.rows;
   if (!direct) {
@@ -907,6 +991,28 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
   else if constexpr (BM == 16) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 8>), eg, block, 0, st, g);
 }
 
+// Tiles of `height` rows if the rows are spread evenly over the slots.
+static long likely_tiles(const LoraArgs& g, int height) {
+  const long spread = (long)g.rows / height + g.slots;
+  return spread < g.rows ? spread : g.rows;
+}
+
+static void launch_lora_fused16(LoraArgs g, hipStream_t st) {
+  int n = 1, rank = 8;
+  long columns = 0;  // of all problems
+  for (int i = 0; i < g.count; ++i) {
+    n = g.p[i].n > n ? g.p[i].n : n;
+    rank = g.p[i].rank > rank ? g.p[i].rank : rank;
+    columns += g.p[i].n;
+  }
+  const long per = (columns * likely_tiles(g, 16) / 512 + 511) / 512 * 512;
+  g.columns = (int)(per < 512 ? 512 : per < 4096 ? per : 4096);
+  const dim3 grid((unsigned)up(g.tiles, kXcds), (n + g.columns - 1) / g.columns, g.count), block(kFewThreads);
+  if (rank <= 16) hipLaunchKernelGGL(lora_fused16_kernel<1>, grid, block, 0, st, g);
+  else if (rank <= 32) hipLaunchKernelGGL(lora_fused16_kernel<2>, grid, block, 0, st, g);
+  else hipLaunchKernelGGL(lora_fused16_kernel<4>, grid, block, 0, st, g);
+}
+
 template <bool ROUTED>
 static void launch_lora_few(LoraArgs g, hipStream_t st) {
   int n = 1, rank = 8;
@@ -918,7 +1024,7 @@ static void launch_lora_few(LoraArgs g, hipStream_t st) {
   }
   const int units = rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 ? 4 : 8;
   const int turn = kFewWaves * 4 * 64 / units;  // columns of a workgroup's turn
-  long per = (columns * g.rows + 255) / 256;    // one workgroup a CU
+  long per = (columns * likely_tiles(g, kFewRows) + 255) / 256;  // one workgroup a CU
   per = (per + turn - 1) / turn * turn;
   g.columns = (int)(per < 4096 ? per : 4096);
   const dim3 grid((unsigned)(ROUTED ? up(g.tiles, kXcds) : g.rows), (n + g.columns - 1) / g.columns, g.count), block(kFewThreads);
@@ -942,6 +1048,7 @@ hipError_t launch_lora(const LoraArgs& g, hipStream_t st) {
   if (g.chunks > 1) hipLaunchKernelGGL(lora_count_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);
   hipLaunchKernelGGL(lora_place_kernel, dim3(g.chunks), dim3(kRouteThreads), 0, st, g);
   if (g.tile_rows == kFewRows) launch_lora_few<true>(g, st);
+  else if (g.way == kLoraRouted16) launch_lora_fused16(g, st);
   else if (g.tile_rows == 64) launch_lora_products<true, 64>(g, st);
   else launch_lora_products<true, 16>(g, st);
   return hipGetLastError();

@@ -192,7 +192,7 @@ constexpr int kLoraMaxSlots = 4096;     // adapters x experts: one LDS counter e
 constexpr int kLoraMaxRank = 256;
 constexpr int kLoraFewRows = 512;       // rows up to which a workgroup of 512 finds its tile itself
 constexpr int kLoraDirectRows = 256;    // and one of 256
-enum { kLoraFew, kLoraDirect, kLoraRouted };
+enum { kLoraFew, kLoraDirect, kLoraRouted, kLoraRouted16 };
 constexpr int kLoraPlanHeader = 8;      // words before the sorted rows
 constexpr int kLoraCountWords = 65536;  // chunks x buckets at most
 constexpr int kLoraChunkMin = 1024;     // rows a chunk at least
