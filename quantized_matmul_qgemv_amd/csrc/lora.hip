@@ -458,7 +458,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs g) {
 // issued before.
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / 64;
-constexpr int kFewRows = 4;
+constexpr int kFewRows = 2;
 
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ float lane_add(float v) {
@@ -480,7 +480,7 @@ __device__ __forceinline__ float sum_to_last(float v) {
 template <int U, int NR>
 __device__ __forceinline__ void few_rows_shrink(const LoraArgs& g, const LoraProblem& p, const TileRows<kFewRows>& tile,
                                                 float (*v)[64]) {
-  constexpr int UK = NR > 1 ? (U <= 2 ? 2 : 1) : U <= 2 ? 4 : U == 4 ? 2 : 1;  // steps of 512 values of k in flight
+  constexpr int UK = U <= 2 ? 4 / NR : U == 4 && NR == 1 ? 2 : 1;  // steps of 512 values of k in flight
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
   const int ranks = p.rank >> 3;
@@ -638,7 +638,6 @@ __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(LoraArgs g) {
     return;
   }
   if (tile.count == 1) few_rows<U, 1>(g, p, tile, first, end, vs);
-  else if (tile.count == 2) few_rows<U, 2>(g, p, tile, first, end, vs);
   else few_rows<U, kFewRows>(g, p, tile, first, end, vs);
 }
 
@@ -896,10 +895,10 @@ static long lora_tiles(int rows, int tile_rows, int slots) {
 //     9728: 1.2 MB); 256 rows of rank 64 (2560, 4096): 35.1 / 29.8, of rank
 //     32: 20.2 / 22.3; 512 rows of rank 16 against sorted ones (1024, 1024):
 //     9.7 / 13.9.  Hence A up to 640 KB and rows x rank up to 8192.
-//   sorted rows, tiles of 4 for dot products against tiles of 16 (768,
-//     2048): rank 8 with 8 rows a slot 32.4 / 37.9, rank 16 with 4 24.7 / 34.0
-//     and with 8 41.1 / 39.3, rank 32 with 2 27.3 / 32.3 and with 4 40.4 /
-//     37.8, rank 64 with 2 47.9 / 47.9.  Hence rows x rank up to 96 a slot.
+//   sorted rows, tiles of 2 for dot products against fused tiles of 16 (768,
+//     2048): rank 8 with 4 rows a slot 20.4 / 21.7 and with 8 35.5 / 27.7,
+//     rank 16 with 2 18.3 / 21.7 and with 4 24.8 / 24.2, rank 32 with 1
+//     37.6 / 36.3 and with 2 30.2 / 24.9.  Hence rows x rank up to 48 a slot.
 //   sorted rows in tiles of 16, one launch of both products against two (4096
 //     pairs on 512 slots): 28.5 / 33.7 (rank 16, 768, 2048), 53.2 / 57.5
 //     (rank 64, 768, 2048: A of 96 KB), 36.4 / 37.2 (rank 32, 2048, 768),
@@ -919,7 +918,7 @@ size_t lora_layout(LoraArgs& g) {
           : g.rows <= kLoraDirectRows                              ? kLoraDirect
                                                                    : kLoraRouted;
   const bool direct = g.way == kLoraFew || g.way == kLoraDirect;
-  g.tile_rows = !direct && small && (long)g.rows * rank <= 96L * g.slots            ? kFewRows
+  g.tile_rows = !direct && small && (long)g.rows * rank <= 48L * g.slots                   ? kFewRows
                 : direct || rank > 128 || g.rows < 24 * g.slots || g.rows < 1024 ? 16
                                                                                   : 64;
   if (!direct && g.tile_rows == 16 && rank <= 64 && a_bytes <= 128 * 1024) g.way = kLoraRouted16;

@@ -148,10 +148,11 @@ SIZES = [
     # A too large for one launch
     (5, 9728, 80, 64, 3, "mixed"),
     (200, 10240, 40, 40, 2, "holes"),
-    # sorted, tiles of 4
+    # sorted, tiles of 2 and of 16
     (1030, 128, 200, 32, 900, "mixed"),
     (700, 192, 65, 64, 700, "holes"),
     (600, 256, 140, 24, 500, "bad"),
+    (520, 64, 40, 64, 1000, "mixed"),
     # sorted, tiles of 64: every rank's kernel, k split and not, several turns of columns
     (1100, 1088, 301, 128, 2, "holes"),
     (1500, 704, 600, 64, 3, "runs"),
