@@ -350,7 +350,7 @@ __device__ __forceinline__ void load_own(float (&v)[V], const float* p, int e0, 
 }
 
 template <int V, int K, bool SCORED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V > 16 ? 2 : 4))) void moe_topk_row_kernel(TopkArgs a) {
+__global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
   extern __shared__ double choices[];  // [4][e], for exact_row with groups
   const int li = threadIdx.x & 15;
   const int wave = threadIdx.x >> 6;
@@ -539,7 +539,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V > 16 ? 2 
         double next = -__builtin_inf();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const double d = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, (double)c[i]) | (uint64_t)(li << 5 | i));
+          float v = c[i];
+          asm volatile("" : "+v"(v));  // formed here: 16 doubles held over the loop would cost 32 registers
+          const double d = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, (double)v) | (uint64_t)(li << 5 | i));
           if (d < below) next = fmax(next, d);
         }
         below = row_max(next);
