@@ -960,12 +960,14 @@ size_t lora_layout(LoraArgs& g) {
 template <bool ROUTED, int BM>
 static void launch_lora_products(LoraArgs g, hipStream_t st) {
   int shrink_y = 1, rank = 1, n = 1;
+  long blocks = 0;  // tiles x 256 columns of all problems
   for (int i = 0; i < g.count; ++i) {
     const LoraProblem& p = g.p[i];
     const int y = p.splits * ((p.rank + 63) / 64);
     shrink_y = y > shrink_y ? y : shrink_y;
     rank = p.rank > rank ? p.rank : rank;
     n = p.n > n ? p.n : n;
+    blocks += (long)((p.n + 255) / 256) * ((g.rows + BM - 1) / BM);
   }
   const unsigned tiles = (unsigned)(ROUTED ? up(g.tiles, kXcds) : g.tiles);
   const dim3 block(kLoraThreads);
@@ -979,10 +981,12 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
     else if (rank <= 32) hipLaunchKernelGGL((lora_shrink16_kernel<ROUTED, 2>), sg, block, 0, st, g);
     else hipLaunchKernelGGL((lora_shrink16_kernel<ROUTED, 4>), sg, block, 0, st, g);
   }
-  // a workgroup's columns: 256, more where there are workgroups enough
-  const long blocks = (long)((n + 255) / 256) * ((g.rows + BM - 1) / BM);
-  const int turns = blocks >= 16384 ? 8 : blocks >= 8192 ? 4 : blocks >= 4096 ? 2 : 1;
-  g.columns = 256 * turns;
+  // A workgroup's columns.  256 against 512 at once (calls of rank 16, k 2560):
+  // 2048 rows, 4096 + 1024 + 1024 columns (768 blocks) 31.5 / 40.4 us; 9728
+  // columns (1216) 46.0 / 45.0; 9728 + 9728 (2432) 77.7 / 72.7; 8192 rows,
+  // 4096 + 1024 + 1024 (3072) 100.3 / 97.4.  Over 512 the last workgroups of
+  // a launch run alone for too long (1280: 86.9 and 112.2).
+  g.columns = blocks >= 1024 ? 512 : 256;
   const dim3 eg(tiles, (n + g.columns - 1) / g.columns, g.count);
   if (rank <= 32) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 1>), eg, block, 0, st, g);
   else if (rank <= 64) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 2>), eg, block, 0, st, g);
