@@ -88,6 +88,8 @@ __device__ __forceinline__ float wave_max(float v) {
 // ---------------------------------------------------------------- exact row
 // One token by a whole wave, in 64 bits: lane i holds experts i, i + 64, ...
 // (V of them), and top_k rounds of a maximum over the wave pick the experts.
+// Bound by its 64-bit exponentials and the latency of its rounds: 110 us for
+// 32768 x 768 (top-8 by logit), 70 us for 32768 x 160 in 5 groups.
 // `choices`: e doubles of LDS of this wave's own (used with groups).
 template <int V>
 __device__ void exact_row(const TopkArgs& a, long tok, double* choices) {
@@ -232,6 +234,13 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_wave_kernel(TopkArgs
 //     any is dropped, and after the merge all experts that are no further
 //     than that below the last chosen one, one for each lane.
 // Rows with a NaN, an infinity or more than 16 such experts go to exact_row.
+//
+// Bound by vector instructions (about 1000 for four tokens where scores are
+// compared, 700 by logit), small calls by latency.  Against a whole wave
+// per token in 64 bits: 1 x 128 top-8 2.7 / 9.9 us, 2048 x 128 3.9 / 12.8,
+// 32768 x 256 by logit 12.9, by sigmoid and bias 16.3, in 8 groups 21 / 147
+// (1.7 TB/s of logits).  Sixteen lanes, as a row's exchanges are single DPP
+// moves and four tokens share every instruction.
 constexpr int kRowTokens = 16;  // tokens per workgroup of 256
 
 template <typename F>
