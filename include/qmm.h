@@ -377,7 +377,7 @@ int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, fl
  * adapters * max(1, experts) (only k and rank of the problems are read; 0 for
  * sizes that are refused), 16-byte aligned, contents on entry do not matter;
  * calls (and captured graphs) that share one must not run concurrently.
- * Up to 256 rows: two launches; more: one or two before them sort the rows by s.
+ * One to four launches, by the sizes alone.
  * t = 0 does nothing.
  * Errors: INVALID_ARG, WORKSPACE, HIP. */
 typedef struct {

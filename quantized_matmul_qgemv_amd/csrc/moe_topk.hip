@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_wave_kernel(TopkArgs
 //     than that below the last chosen one, one for each lane.
 // Rows with a NaN, an infinity or more than 16 such experts go to exact_row.
 //
-// Bound by vector instructions (about 1000 for four tokens where scores are
+// Bound by vector instructions (about 1100 for four tokens where scores are
 // compared, 700 by logit), small calls by latency.  Against a whole wave
 // per token in 64 bits: 1 x 128 top-8 2.7 / 9.9 us, 2048 x 128 3.9 / 12.8,
 // 32768 x 256 by logit 12.9, by sigmoid and bias 16.3, in 8 groups 21 / 147
