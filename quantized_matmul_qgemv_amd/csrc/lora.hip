@@ -641,9 +641,11 @@ template <bool ROUTED, int U>
 __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(LoraArgs g) {
   __shared__ TileRows<kFewRows> tile;
   __shared__ float vs[kFewRows][64];
-  const LoraProblem& p = g.p[blockIdx.z];
-  const int first = blockIdx.y * g.columns;
-  if (first >= p.n) return;
+  // the grid's second dimension counts the column ranges of all problems
+  int problem = 0;
+  while (problem + 1 < g.count && (int)blockIdx.y >= g.first_range[problem + 1]) ++problem;
+  const LoraProblem& p = g.p[problem];
+  const int first = ((int)blockIdx.y - g.first_range[problem]) * g.columns;
   if (!(ROUTED ? read_tile(g, blockIdx.x, tile) : find_tile<kFewThreads>(g, blockIdx.x, tile))) return;
   const int end = first + g.columns < p.n ? first + g.columns : p.n;
   if (tile.slot < 0) {
@@ -999,8 +1001,8 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
   // A workgroup's columns.  256 against 512 at once (calls of rank 16, k 2560):
   // 2048 rows, 4096 + 1024 + 1024 columns (768 blocks) 31.5 / 40.4 us; 9728
   // columns (1216) 46.0 / 45.0; 9728 + 9728 (2432) 77.7 / 72.7; 8192 rows,
-  // 4096 + 1024 + 1024 (3072) 100.3 / 97.4.  Over 512 the last workgroups of
-  // a launch run alone for too long (1280: 86.9 and 112.2).
+  // 4096 + 1024 + 1024 columns 100.3 / 97.4.  Over 512 the last workgroups of a
+  // launch run alone for too long (1280: 86.9 and 112.2).
   g.columns = blocks >= 1024 ? 512 : 256;
   const dim3 eg(tiles, (n + g.columns - 1) / g.columns, g.count);
   if (rank <= 32) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 1>), eg, block, 0, st, g);
@@ -1009,7 +1011,7 @@ static void launch_lora_products(LoraArgs g, hipStream_t st) {
   else if constexpr (BM == 16) hipLaunchKernelGGL((lora_expand_kernel<ROUTED, BM, 8>), eg, block, 0, st, g);
 }
 
-// Tiles of `height` rows if the rows are spread evenly over the slots.
+// Tiles of `height` rows, at most: whole ones and a last one of each slot.
 static long likely_tiles(const LoraArgs& g, int height) {
   const long spread = (long)g.rows / height + g.slots;
   return spread < g.rows ? spread : g.rows;
@@ -1033,10 +1035,9 @@ static void launch_lora_fused16(LoraArgs g, hipStream_t st) {
 
 template <bool ROUTED>
 static void launch_lora_few(LoraArgs g, hipStream_t st) {
-  int n = 1, rank = 8;
+  int rank = 8, ranges = 0;
   long columns = 0;  // of all problems
   for (int i = 0; i < g.count; ++i) {
-    n = g.p[i].n > n ? g.p[i].n : n;
     rank = g.p[i].rank > rank ? g.p[i].rank : rank;
     columns += g.p[i].n;
   }
@@ -1045,7 +1046,11 @@ static void launch_lora_few(LoraArgs g, hipStream_t st) {
   long per = (columns * likely_tiles(g, kFewRows) + 255) / 256;  // one workgroup a CU
   per = (per + turn - 1) / turn * turn;
   g.columns = (int)(per < 4096 ? per : 4096);
-  const dim3 grid((unsigned)(ROUTED ? up(g.tiles, kXcds) : g.rows), (n + g.columns - 1) / g.columns, g.count), block(kFewThreads);
+  for (int i = 0; i < g.count; ++i) {
+    g.first_range[i] = ranges;
+    ranges += (g.p[i].n + g.columns - 1) / g.columns;
+  }
+  const dim3 grid((unsigned)(ROUTED ? up(g.tiles, kXcds) : g.rows), ranges), block(kFewThreads);
   switch (units) {
     case 1: hipLaunchKernelGGL((lora_few_kernel<ROUTED, 1>), grid, block, 0, st, g); break;
     case 2: hipLaunchKernelGGL((lora_few_kernel<ROUTED, 2>), grid, block, 0, st, g); break;

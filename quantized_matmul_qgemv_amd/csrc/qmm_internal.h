@@ -217,6 +217,7 @@ struct LoraArgs {
   size_t plan_tiles, plan_counts;
   int32_t count, rows, top_k, adapters, experts, slots;
   int32_t way, tile_rows, columns, chunk, chunks;
+  int32_t first_range[kLoraMaxProblems];  // of the column ranges of all problems, a problem's first
   int64_t tiles;  // most tiles that the rows can form
 };
 size_t lora_layout(LoraArgs& g);
