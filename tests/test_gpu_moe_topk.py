@@ -86,6 +86,20 @@ CASES = [
     (13, 384, 8, dict(score="sigmoid", bias=True, scale=2.827)),
     (6, 16, 16, dict(score="sigmoid", groups=2, group_keep=2, group_top=2)),
     (1009, 72, 6, dict(groups=4, group_keep=2, bias=True)),
+    # every list length with every number of experts a lane holds, by logit and by score
+    (31, 50, 12, {}),
+    (31, 50, 12, dict(bias=True)),
+    (18, 120, 16, {}),
+    (18, 120, 11, dict(score="sigmoid", bias=True)),
+    (15, 200, 16, {}),
+    (15, 256, 16, dict(bias=True)),
+    (15, 300, 12, dict(renormalize=False)),
+    (15, 500, 16, dict(score="sigmoid", bias=True)),
+    (15, 400, 8, dict(bias=True)),
+    (15, 512, 8, dict(groups=16, group_keep=3)),
+    (15, 512, 8, dict(groups=2, group_keep=1, group_top=2, score="sigmoid")),
+    (4, 513, 8, dict(bias=True)),
+    (4, 100, 17, dict(score="sigmoid", bias=True)),
 ]
 
 
