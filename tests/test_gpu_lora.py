@@ -199,15 +199,19 @@ def test_experts(t, top_k, experts, adapters, per_pair):
     check(flat, x, a, b, ids, "flattened", **kw)
 
 
-@pytest.mark.parametrize("t", [40, 600])
-def test_batched_projections(t):
+@pytest.mark.parametrize("t, adapters, last", [
+    (40, 6, 128), (600, 6, 128), (1600, 6, 128),  # two products a call: tiles by ballots, sorted tiles of 16 and of 64
+    (40, 6, 24), (100, 90, 24), (600, 900, 24), (600, 6, 24),  # one launch: dot products, the same over sorted rows, tiles of 16
+])
+def test_batched_projections(t, adapters, last):
     """Problems of one call: other inputs, widths and ranks; each as if alone."""
-    say("lora batched", t)
-    r = np.random.default_rng([83, t])
-    ids = some_ids(r, t, 6, "holes")
+    say("lora batched", t, adapters, last)
+    r = np.random.default_rng([83, t, adapters, last])
+    ids = some_ids(r, t, adapters, "holes")
     parts = []
-    for k, n, rank, with_base in [(320, 200, 16, True), (320, 33, 64, False), (128, 1, 8, True), (1088, 64, 128, True)]:
-        a, b = weights(r, 6, rank, k, n)
+    for k, n, rank, with_base in [(320, 200, 16, True), (320, 33, 64, False), (128, 1, 8, True), (704, 64, last, True),
+                                  (64, 2100, 8, False)]:
+        a, b = weights(r, adapters, rank, k, n)
         x = r.standard_normal((t, k)).astype(np.float16)
         parts.append((x, a, b, r.standard_normal((t, n)).astype(np.float32) if with_base else None))
     I = dev(ids)
