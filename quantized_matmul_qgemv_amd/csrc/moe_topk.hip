@@ -227,12 +227,16 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_wave_kernel(TopkArgs
 //     the logit and below them 1023 - expert: equal logits order by the
 //     lower expert.
 //   SCORED: the fp32 choice as a double, its place (lane, element) in the 29
-//     bits that are free.  The fp32 choice is off by at most
+//     bits that are free.  By sigmoid the fp32 choice is off by at most
 //     2^-21 + 2^-23 |c| (exp2 and rcp to one unit; the rounded argument's
-//     part: |l| s (1 - s) < 0.28).  Where two that matter are nearer than
-//     twice that, they are formed again in 64 bits: the groups' scores before
-//     any is dropped, and after the merge all experts that are no further
-//     than that below the last chosen one, one for each lane.
+//     part: |l| s (1 - s) < 0.28).  By softmax all scores of a row share the
+//     error of the sum (36 additions, 2^-24 each; the exponentials' errors
+//     weighted by their scores, below 9 * 2^-24; rcp), in all 50 * 2^-24 of the
+//     difference of two scores, which is below 0.8 * 2^-18.  Choices that
+//     matter and are nearer than kNear (twice that by softmax) + 2^-21 |c|,
+//     which covers both errors of a pair, are formed again in 64 bits: the
+//     groups' scores before any is dropped, and after the merge all experts
+//     that are no further than that below the last chosen one, one for each lane.
 // Rows with a NaN, an infinity or more than 16 such experts go to exact_row.
 //
 // Bound by vector instructions (about 1100 for four tokens where scores are
@@ -242,6 +246,7 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_wave_kernel(TopkArgs
 // (1.7 TB/s of logits).  Sixteen lanes, as a row's exchanges are single DPP
 // moves and four tokens share every instruction.
 constexpr int kRowTokens = 16;  // tokens per workgroup of 256
+constexpr float kNear = 0x1p-19f;
 
 template <typename F>
 __device__ __forceinline__ float row_all(float v, F f) {
@@ -375,6 +380,7 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
   const bool whole = (per & 3) == 0 && a.e == per * 16;
   load_own<V>(l, row, e0, own, a.e, per, whole && ((uintptr_t)a.logits & 15) == 0, -inf);
 
+  const float near_by = a.score == 0 ? 2 * kNear : kNear;
   bool slow = false;
   float c[V];  // choices
   float top = -inf;
@@ -460,8 +466,9 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
       kept = lanes_before((double)g, li / lanes) < most;
     } else {
       kept = groups_before(g, lanes) * lanes < most;  // nearly equal ones are told apart below
-      const float err = a.group_top == 1 ? 0x1p-20f + 0x1p-22f * fabsf(first)
-                                         : 0x1p-19f + 0x1p-22f * (fabsf(first) + fabsf(second));
+      // of one group: half of what a pair of choices may differ by, for each choice in it
+      const float err = a.group_top == 1 ? 0.5f * near_by + 0x1p-22f * fabsf(first)
+                                         : near_by + 0x1p-22f * (fabsf(first) + fabsf(second));
       const uint32_t keeping = (uint32_t)(__ballot(kept) >> (threadIdx.x & 48)) & 0xFFFF;  // too many where some are equal
       const bool near = __popc(keeping) != most ||
                         !(row_all(kept ? g - err : inf, min_f) > row_all(kept ? -inf : g + err, max_f));
@@ -528,7 +535,7 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
   int id = expert_of(got);
   if constexpr (SCORED) {
     const float v = (float)got;
-    const float err = 0x1p-19f + 0x1p-21f * fabsf(v);
+    const float err = near_by + 0x1p-21f * fabsf(v);
     // the lane before holds the next larger one (row_shr:1)
     const float before = dpp_f<0x111>(v);
     bool near = li > 0 && li < a.top_k && !(before - v > err);
