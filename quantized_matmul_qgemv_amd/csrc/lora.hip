@@ -507,20 +507,18 @@ __device__ __forceinline__ void few_rows_shrink(const LoraArgs& g, const LoraPro
   for (int i = 0; i < U; ++i)
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[i][r] = 0.0f;
-  for (int k0 = lane * 8; k0 < p.k + lane * 8; k0 += 512 * UK) {
-    u32x4 a[UK][U], x[UK][NR];
+  // Lanes past the end of k load nothing: they leave the loop, or have zeros
+  // for both A and x (an infinity loaded in their place, times zero, is NaN).
+  for (int k0 = lane * 8; k0 < p.k; k0 += 512 * UK) {
+    u32x4 a[UK][U] = {}, x[UK][NR] = {};
 #pragma unroll
     for (int u = 0; u < UK; ++u) {
       const int k = k0 + u * 512;
-      const bool in = k < p.k;
-      const int at = in ? k : 0;
+      if (u > 0 && k >= p.k) break;
 #pragma unroll
-      for (int i = 0; i < U; ++i) a[u][i] = *(gptr<u32x4>)(ap + (size_t)(i < ranks ? i : 0) * p.k + at);
+      for (int i = 0; i < U; ++i) a[u][i] = *(gptr<u32x4>)(ap + (size_t)(i < ranks ? i : 0) * p.k + k);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        x[u][r] = *(gptr<u32x4>)(xp[r] + at);
-        if (!in) x[u][r] = u32x4{0, 0, 0, 0};
-      }
+      for (int r = 0; r < NR; ++r) x[u][r] = *(gptr<u32x4>)(xp[r] + k);
     }
 #pragma unroll
     for (int u = 0; u < UK; ++u)
