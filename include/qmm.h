@@ -336,7 +336,8 @@ int qmm_moe_combine(const float* y_pairs, const float* weights, float* y, int t,
  *   groups: divides E, at most 64 (1: no groups, then group_keep = 1);
  *   top_k: at most 64 and at most the experts of group_keep groups;
  *   E at most 1024; T below 2^26.
- * One launch, no workspace.  t = 0 does nothing.
+ * One launch (of 2^26 - 3 tokens and more it can be two), no workspace.  t = 0
+ * does nothing.
  * Errors: INVALID_ARG, UNSUPPORTED (score), HIP. */
 #define QMM_SCORE_SOFTMAX 0
 #define QMM_SCORE_SIGMOID 1

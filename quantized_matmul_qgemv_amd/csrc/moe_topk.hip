@@ -601,6 +601,8 @@ __global__ __launch_bounds__(256) void moe_topk_row_kernel(TopkArgs a) {
   }
 }
 
+static_assert((kTopkTokens + kRowTokens - 1L) / kRowTokens * 256 < 1L << 32, "the threads of a launch");
+
 template <int V, int K>
 static void launch_row(const TopkArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(((long)a.t + kRowTokens - 1) / kRowTokens)), block(256);
@@ -609,11 +611,23 @@ static void launch_row(const TopkArgs& a, hipStream_t st) {
   else hipLaunchKernelGGL((moe_topk_row_kernel<V, K, false>), grid, block, lds, st, a);
 }
 
+// A launch has fewer than 2^32 threads, which the last tokens of the largest
+// calls would make in whole workgroups: those take a launch of their own (a
+// loop over tokens in the kernel instead: 163 registers for 78).
 template <int V>
 static void launch_wave(const TopkArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(((long)a.t + kTopkWaves - 1) / kTopkWaves)), block(kTopkWaves * 64);
+  constexpr int most = 0xFFFFFFFFu / (kTopkWaves * 64) * kTopkWaves;
+  const dim3 block(kTopkWaves * 64);
   const size_t lds = a.groups > 1 ? (size_t)kTopkWaves * a.e * sizeof(double) : 0;
-  hipLaunchKernelGGL(moe_topk_wave_kernel<V>, grid, block, lds, st, a);
+  for (int first = 0; first < a.t; first += most) {
+    TopkArgs part = a;
+    part.logits += (size_t)first * a.e;
+    part.ids += (size_t)first * a.top_k;
+    part.weights += (size_t)first * a.top_k;
+    part.t = a.t - first < most ? a.t - first : most;
+    const dim3 grid((unsigned)(((long)part.t + kTopkWaves - 1) / kTopkWaves));
+    hipLaunchKernelGGL(moe_topk_wave_kernel<V>, grid, block, lds, st, part);
+  }
 }
 
 // Sixteen lanes a token where a lane's experts fit its registers, the list of

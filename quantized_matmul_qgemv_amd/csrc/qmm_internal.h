@@ -170,7 +170,7 @@ hipError_t launch_moe_combine(const float* y_pairs, const float* weights, float*
                               int n, hipStream_t st);
 
 // Choice of experts from router logits (moe_topk.hip).
-constexpr int kTopkTokens = (1 << 26) - 1;  // tokens: 64 lanes each within one grid dimension's 2^32
+constexpr int kTopkTokens = (1 << 26) - 1;  // tokens a call
 constexpr int kTopkMax = 64;    // experts per token: one lane each
 constexpr int kGroupsMax = 64;  // expert groups: one bit each
 struct TopkArgs {
