@@ -361,13 +361,14 @@ int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, fl
  *   base  fp32 [t * top_k, n], the shared product; it may be y itself (added
  *         in place) or NULL (y is the adapters' part alone), but must not
  *         overlap y otherwise
- *   y     fp32 [t * top_k, n], overwritten
+ *   y     fp32 [t * top_k, n], overwritten; must not overlap x
  *   adapter_ids  [t] int32; -1: no adapter, the row is base (0 without base)
  *   scales       [adapters] fp32 (alpha / rank), or NULL for 1
  * An adapter id below -1 or >= adapters, or an expert id outside
  * [0, experts) of a row with an adapter, makes the row NaN.
  * The up to 8 problems of one call (q, k and v; gate and up) share the ids and
- * run in the same launches; their y must not overlap.  Adapters of smaller
+ * run in the same launches: no y may overlap another problem's y, base or x
+ * (two adapters on one output are two calls).  Adapters of smaller
  * rank are padded with zeros to the problem's rank, a multiple of 8 up to
  * 256; k is a multiple of 64 up to 2^24, adapters x experts at most 4096, n at most
  * 2097152, t * top_k at most 2^27.  A B x is held in fp32 throughout (products of fp16, A x exact to

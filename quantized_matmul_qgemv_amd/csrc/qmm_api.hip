@@ -98,6 +98,29 @@ int check_lora_sizes(const char* fn, const qmm_lora_problem& q, int i) {
   return QMM_OK;
 }
 
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  return (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
+}
+
+// The problems of a call run together: none may write what another one reads
+// or writes, nor its own x (its own base is checked on its own).
+int check_lora_overlaps(const char* fn, const qmm_lora_problem* problems, int count, int t, int top_k) {
+  const size_t rows = (size_t)t * top_k;
+  for (int i = 0; i < count; ++i) {
+    const qmm_lora_problem& p = problems[i];
+    const size_t y_bytes = rows * p.n * 4;
+    for (int j = 0; j < count; ++j) {
+      const qmm_lora_problem& q = problems[j];
+      const char* what = nullptr;
+      if (j < i && overlap(p.y, y_bytes, q.y, rows * q.n * 4)) what = "y";
+      else if (j != i && q.base != nullptr && overlap(p.y, y_bytes, q.base, rows * q.n * 4)) what = "base";
+      else if (overlap(p.y, y_bytes, q.x, (q.x_row_per_pair ? rows : t) * q.k * 2)) what = "x";
+      if (what) return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: y overlaps the %s of problem %d", fn, i, what, j);
+    }
+  }
+  return QMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -671,9 +694,8 @@ int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter
       return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: x, a or b is not 16-byte aligned", fn, i);
     if (!aligned(q.y, 4) || !aligned(q.base, 4))
       return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: base or y is not 4-byte aligned", fn, i);
-    const uintptr_t y = (uintptr_t)q.y, b = (uintptr_t)q.base;
     const size_t bytes = (size_t)t * top_k * q.n * 4;
-    if (q.base != nullptr && y != b && y < b + bytes && b < y + bytes)
+    if (q.base != nullptr && q.y != q.base && overlap(q.y, bytes, q.base, bytes))
       return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: y overlaps base without being base", fn, i);
     qmm::LoraProblem& p = g.p[i];
     p.x = q.x;
@@ -698,6 +720,7 @@ int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter
   const size_t need = qmm::lora_layout(g);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
+  if (int st = check_lora_overlaps(fn, problems, count, t, top_k)) return st;
   CHECK_PTR(workspace, 16);
   g.v = static_cast<float*>(workspace);
   g.plan = static_cast<int32_t*>(workspace);

@@ -1,0 +1,57 @@
+"""Low-rank adapters without a GPU: calls that cannot be meant are refused, with
+what is meant beside them taken, before any HIP call."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_matmul_qgemv_amd as qmm  # noqa: E402
+from quantized_matmul_qgemv_amd import _lib  # noqa: E402
+from quantized_matmul_qgemv_amd._lib import LoraProblem  # noqa: E402
+from test_lora_cpu import A, INV, Y, call, problem  # noqa: E402
+
+X = 0x80000000  # more fake addresses
+T, N = 4, 64
+ROWS = T * N * 4  # bytes of a y or base
+
+
+# ------------------------------------------------ problems of one call that overlap
+
+@pytest.mark.parametrize("problems, text", [
+    ([problem(), problem()], "problem 1: y overlaps the y of problem 0"),
+    ([problem(), problem(y=Y + ROWS - 4)], "problem 1: y overlaps the y of problem 0"),
+    ([problem(y=Y + ROWS - 4), problem()], "problem 1: y overlaps the y of problem 0"),
+    ([problem(), problem(y=Y + ROWS), problem(y=Y + 2 * ROWS - 4)], "problem 2: y overlaps the y of problem 1"),
+    # two adapters stacked in one call: the second would read what the first has, or has not yet, written
+    ([problem(), problem(base=Y, y=Y + ROWS)], "problem 0: y overlaps the base of problem 1"),
+    ([problem(base=Y + ROWS), problem(y=Y + ROWS)], "problem 1: y overlaps the base of problem 0"),
+    ([problem(), problem(base=Y + ROWS - 4, y=Y + 2 * ROWS)], "problem 0: y overlaps the base of problem 1"),
+    ([problem(x=Y)], "problem 0: y overlaps the x of problem 0"),
+    ([problem(), problem(x=Y + ROWS - 16, y=Y + ROWS)], "problem 0: y overlaps the x of problem 1"),
+    ([problem(x=X), problem(x=X - ROWS + 16, y=X - ROWS + 16)], "problem 1: y overlaps the x of problem 0"),
+])
+def test_problems_that_overlap(problems, text):
+    assert call(problems=problems) == INV, _lib.last_error()
+    assert text in _lib.last_error(), _lib.last_error()
+
+
+@pytest.mark.parametrize("problems", [
+    [problem(), problem(y=Y + ROWS)],
+    [problem(base=Y), problem(base=Y + ROWS, y=Y + ROWS)],             # each in place
+    [problem(base=X), problem(base=X, y=Y + ROWS)],                    # one base of both
+    [problem(x=X), problem(x=X, y=X + T * 64 * 2)],                    # y right behind x
+    [problem(x=X), problem(x=X, y=X - ROWS)],                          # and right before
+    [problem(x=X, x_row_per_pair=0), problem(x=X, y=X + 64 * 64 * 2)],
+])
+def test_problems_side_by_side(problems):
+    """Taken as far as the last check before the launch, the workspace's alignment."""
+    assert call(problems=problems, ws=A + 8) == INV
+    assert "workspace is not 16-byte aligned" in _lib.last_error(), _lib.last_error()
+
+
+def test_the_rows_of_pairs_count():
+    ps = [problem(x=X, x_row_per_pair=1, y=X + T * 64 * 2)]  # x has a row for every pair: twice as many
+    kw = dict(top_k=2, experts=4, experts_ids=A, ws=A + 8)
+    assert call(problems=ps, **kw) == INV
+    assert "problem 0: y overlaps the x of problem 0" in _lib.last_error()
+    assert call(problems=[problem(x=X, x_row_per_pair=0, y=X + T * 64 * 2)], **kw) == INV
+    assert "workspace is not 16-byte aligned" in _lib.last_error()
