@@ -85,12 +85,15 @@ constexpr long kMaxLoraRows = 1 << 27;
 constexpr int kMaxLoraK = 1 << 24;
 constexpr int kMaxLoraN = 1 << 21;  // column blocks of 64 in one grid dimension
 
+bool lora_k(int k) { return k >= 64 && k % 64 == 0 && k <= kMaxLoraK; }
+bool lora_rank(int rank) { return rank >= 8 && rank % 8 == 0 && rank <= qmm::kLoraMaxRank; }
+
 int check_lora_sizes(const char* fn, const qmm_lora_problem& q, int i) {
   if (q.n < 1 || q.n > kMaxLoraN)
     return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: n=%d must be in [1, %d]", fn, i, q.n, kMaxLoraN);
-  if (q.k < 64 || q.k % 64 != 0 || q.k > kMaxLoraK)
+  if (!lora_k(q.k))
     return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: k=%d must be a positive multiple of 64 up to %d", fn, i, q.k, kMaxLoraK);
-  if (q.rank < 8 || q.rank > qmm::kLoraMaxRank || q.rank % 8 != 0)
+  if (!lora_rank(q.rank))
     return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: rank=%d must be a multiple of 8 in [8, %d]", fn, i,
                 q.rank, qmm::kLoraMaxRank);
   if (q.x_row_per_pair != 0 && q.x_row_per_pair != 1)
@@ -654,7 +657,7 @@ size_t qmm_lora_workspace_size(const qmm_lora_problem* problems, int count, int 
   g.rows = rows;
   g.slots = slots;
   for (int i = 0; i < count; ++i) {
-    if (check_lora_sizes("", problems[i], i)) return 0;
+    if (!lora_k(problems[i].k) || !lora_rank(problems[i].rank)) return 0;
     g.p[i].k = problems[i].k;
     g.p[i].rank = problems[i].rank;
   }

@@ -55,3 +55,25 @@ def test_the_rows_of_pairs_count():
     assert "problem 0: y overlaps the x of problem 0" in _lib.last_error()
     assert call(problems=[problem(x=X, x_row_per_pair=0, y=X + T * 64 * 2)], **kw) == INV
     assert "workspace is not 16-byte aligned" in _lib.last_error()
+
+
+# ------------------------------------------------ what the workspace's size depends on
+
+def size(rows, slots, *ps):
+    arr = (LoraProblem * len(ps))(*ps)
+    return _lib.lib().qmm_lora_workspace_size(arr, len(ps), rows, slots)
+
+
+@pytest.mark.parametrize("rows", [4, 300, 5000])
+def test_the_workspace_depends_on_k_and_rank_alone(rows):
+    assert call(t=0) == 0
+    need = size(rows, 8, problem(k=4096, rank=16), problem(k=64, rank=128))
+    assert need > 0
+    bare = [LoraProblem(None, None, None, None, None, 0, 4096, 16, 0), LoraProblem(None, None, None, None, None, -1, 64, 128, 7)]
+    assert size(rows, 8, *bare) == need
+    for bad in (dict(k=0), dict(k=65), dict(rank=0), dict(rank=12), dict(rank=264)):
+        assert size(rows, 8, problem(**bad)) == 0
+        assert _lib.last_error() == ""  # asking for a size is no failed call
+    # the call itself looks at everything
+    assert call(problems=[problem(n=0)]) == INV and "n=0" in _lib.last_error()
+    assert call(problems=[problem(x_row_per_pair=7)]) == INV and "x_row_per_pair" in _lib.last_error()
