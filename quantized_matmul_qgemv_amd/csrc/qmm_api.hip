@@ -687,6 +687,7 @@ int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter
   if (t == 0) return QMM_OK;
   CHECK_PTR(adapter_ids, 4);
   if (experts > 0) CHECK_PTR(expert_ids, 4);
+  else if (expert_ids != nullptr) return fail(QMM_ERR_INVALID_ARG, "%s: expert_ids without experts", fn);
   if (scales != nullptr) CHECK_PTR(scales, 4);
   qmm::LoraArgs g{};
   for (int i = 0; i < count; ++i) {

@@ -77,3 +77,12 @@ def test_the_workspace_depends_on_k_and_rank_alone(rows):
     # the call itself looks at everything
     assert call(problems=[problem(n=0)]) == INV and "n=0" in _lib.last_error()
     assert call(problems=[problem(x_row_per_pair=7)]) == INV and "x_row_per_pair" in _lib.last_error()
+
+
+# ------------------------------------------------ experts that are named in part
+
+def test_expert_ids_without_a_number_of_experts():
+    assert call(experts=0, experts_ids=A, ws=A + 8) == INV
+    assert "expert_ids without experts" in _lib.last_error(), _lib.last_error()
+    assert call(experts=4, experts_ids=A, ws=A + 8) == INV
+    assert "workspace is not 16-byte aligned" in _lib.last_error()
