@@ -386,8 +386,9 @@ def _lora_rows(problems, adapter_ids, expert_ids):
             raise ValueError(f"expert_ids must be [{t}, top_k], not {tuple(expert_ids.shape)}")
         top_k = expert_ids.shape[1]
     shape = problems[0][1].shape
-    if len(shape) < 3:
-        raise ValueError(f"problem 0: a must be [adapters, rank, k], not {tuple(shape)}")
+    if len(shape) != 3 and (len(shape) != 4 or expert_ids is None):
+        raise ValueError("problem 0: a must be [adapters, rank, k]" + (
+            " without expert_ids" if expert_ids is None else " or [adapters, experts, rank, k]") + f", not {tuple(shape)}")
     return t, top_k, shape[0] if len(shape) == 3 else shape[0] * shape[1]
 
 

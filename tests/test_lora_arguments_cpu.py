@@ -86,3 +86,25 @@ def test_expert_ids_without_a_number_of_experts():
     assert "expert_ids without experts" in _lib.last_error(), _lib.last_error()
     assert call(experts=4, experts_ids=A, ws=A + 8) == INV
     assert "workspace is not 16-byte aligned" in _lib.last_error()
+
+
+# ------------------------------------------------ the Python call's shapes
+
+def h(*shape):
+    return torch.zeros(*shape, dtype=torch.float16)
+
+
+IDS, EXPERT_IDS = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32)
+
+
+def test_weights_for_experts_without_expert_ids():
+    """[adapters, experts, ...] weights in a call without expert_ids: not adapters x experts of them."""
+    a, b = h(2, 3, 8, 64), h(2, 3, 10, 8)
+    with pytest.raises(ValueError, match=r"problem 0: a must be \[adapters, rank, k\] without expert_ids"):
+        qmm.lora(h(4, 64), a, b, IDS)
+    with pytest.raises(ValueError, match="without expert_ids"):
+        qmm.lora_workspace([(h(4, 64), a, b, None, None)], IDS)
+    with pytest.raises(ValueError, match="device tensor"):
+        qmm.lora(h(4, 64), a, b, IDS, expert_ids=EXPERT_IDS)
+    with pytest.raises(ValueError, match="device tensor"):
+        qmm.lora(h(4, 64), a[:, 0], b[:, 0], IDS)
