@@ -428,6 +428,11 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
             raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
     if scales is not None and scales.shape != (adapters,):
         raise ValueError(f"scales must be [{adapters}], not {tuple(scales.shape)}")
+    held = ((slots,), (adapters, experts)) if experts else ((slots,),)  # flattened, by adapter and expert
+    for i, (_, a, b, _, _) in enumerate(problems):
+        if a.shape[:-2] not in held or b.shape[:-2] not in held or b.shape[-1] != a.shape[-2]:
+            raise ValueError(f"problem {i}: a {tuple(a.shape)} and b {tuple(b.shape)} must be [{slots}, rank, k] "
+                             f"and [{slots}, n, rank]" + (f", or [{adapters}, {experts}, ...]" if experts else ""))
     rows, per_pair = t * top_k, 1 if x_row_per_pair else 0
     x_rows = rows if per_pair else t
     d, checked, out = None, [], []
@@ -436,9 +441,6 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
         n = b.shape[-2]
         if x.shape != (x_rows, k):
             raise ValueError(f"problem {i}: x must be [{x_rows}, {k}], not {tuple(x.shape)}")
-        if a.numel() != slots * rank * k or b.shape[-1] != rank or b.numel() != slots * n * rank:
-            raise ValueError(f"problem {i}: a {tuple(a.shape)} and b {tuple(b.shape)} must be [{slots}, rank, k] "
-                             f"and [{slots}, n, rank]")
         if base is not None and base.shape != (rows, n):
             raise ValueError(f"problem {i}: base must be [{rows}, {n}], not {tuple(base.shape)}")
         if y is None:

@@ -108,3 +108,30 @@ def test_weights_for_experts_without_expert_ids():
         qmm.lora(h(4, 64), a, b, IDS, expert_ids=EXPERT_IDS)
     with pytest.raises(ValueError, match="device tensor"):
         qmm.lora(h(4, 64), a[:, 0], b[:, 0], IDS)
+
+
+def test_weights_laid_out_otherwise():
+    """Every a and b holds its weights by adapter and expert as the call has them;
+    an equal number of values is not enough."""
+    x, a, b = h(4, 64), h(2, 3, 8, 64), h(2, 3, 10, 8)
+    kw = dict(expert_ids=EXPERT_IDS)
+    flat_a, flat_b, scales = h(6, 8, 64), h(6, 10, 8), torch.ones(2)
+    for args, other in [
+        ((x, a, h(3, 2, 10, 8), IDS), kw),              # b by expert and adapter
+        ((x, a, h(6, 1, 10, 8), IDS), kw),
+        ((x, a, h(2, 3, 1, 10, 8), IDS), kw),
+        ((x, h(2, 8, 64), h(2, 1, 10, 8), IDS), {}),
+        ((x, h(2, 8, 64), h(2, 0, 10, 8), IDS), {}),
+        ((x, flat_a, h(3, 2, 10, 8), IDS), dict(kw, scales=scales)),
+    ]:
+        with pytest.raises(ValueError, match="problem 0: a .* and b .* must be"):
+            qmm.lora(*args, **other)
+    for second in [(x, h(3, 2, 8, 64), b, None, None), (x, h(3, 2, 8, 64), h(3, 2, 10, 8), None, None),
+                   (x, h(2, 8, 64), h(2, 10, 8), None, None)]:
+        with pytest.raises(ValueError, match="problem 1: a .* and b .* must be"):
+            qmm.lora_batched([(x, a, b, None, None), second], IDS, **kw)
+    # each way of holding the same weights, and both in one call
+    for args, other in [((x, a, b, IDS), kw), ((x, a, flat_b, IDS), kw), ((x, flat_a, flat_b, IDS), dict(kw, scales=scales)),
+                        ((x, flat_a, b, IDS), dict(kw, scales=scales))]:
+        with pytest.raises(ValueError, match="device tensor"):
+            qmm.lora(*args, **other)
