@@ -392,6 +392,26 @@ def _lora_rows(problems, adapter_ids, expert_ids):
     return t, top_k, shape[0] if len(shape) == 3 else shape[0] * shape[1]
 
 
+def _lora_experts(problems, slots, scales, expert_ids, experts):
+    """The number of experts of a call (0 without expert_ids): as given, of
+    weights that are not flattened, or by the number of scales."""
+    if expert_ids is None:
+        if experts is not None:
+            raise ValueError(f"experts={experts} without expert_ids")
+        return 0
+    if experts is not None:
+        if experts < 1:
+            raise ValueError(f"experts={experts} must be positive")
+        return experts
+    for _, a, b, _, _ in problems:
+        for w in (a, b):
+            if w.dim() == 4:
+                return w.shape[1]
+    if scales is None or scales.numel() == 0:
+        raise ValueError("a must be [adapters, experts, rank, k] (or experts, or scales [adapters], be given)")
+    return slots // scales.numel()
+
+
 def lora_workspace(problems, adapter_ids, expert_ids=None, stream=None):
     """A workspace for lora and lora_batched calls of these sizes (kept by the
     caller; calls that share one must not overlap in time)."""
@@ -404,28 +424,21 @@ def lora_workspace(problems, adapter_ids, expert_ids=None, stream=None):
 
 
 def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_pair: bool = False,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, experts=None):
     """y = base + scales[id] * B_id (A_id x) for the projections of one input
     (q, k and v; gate and up) in the same launches, via qmm_lora: a list of
     (x, a, b, base, y) with base None, or y itself to add in place.
     adapter_ids int32 [T], -1 for no adapter; a [adapters, rank, k] and
     b [adapters, n, rank] fp16.  With expert_ids [T, top_k] the rows are the
-    pairs of a routed layer and each adapter has weights for every expert
-    ([adapters, experts, ...], or flattened with scales given).  Returns the
-    list of y."""
+    pairs of a routed layer and each adapter has weights for every expert:
+    [adapters, experts, ...], or flattened to [adapters * experts, ...], where
+    `experts` says how many (without it scales do, by being [adapters]: give
+    it to have their length checked).  Returns the list of y."""
     t, top_k, slots = _lora_rows(problems, adapter_ids, expert_ids)
-    a = problems[0][1]
-    experts, adapters = 0, slots
-    if expert_ids is not None:
-        if a.dim() == 4:
-            experts = a.shape[1]
-        elif scales is not None and scales.numel() > 0:
-            experts = slots // scales.numel()
-        else:
-            raise ValueError("a must be [adapters, experts, rank, k] (or scales [adapters] be given)")
-        adapters = slots // max(1, experts)
-        if adapters * experts != slots:
-            raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
+    experts = _lora_experts(problems, slots, scales, expert_ids, experts)
+    adapters = slots // max(1, experts)
+    if experts and adapters * experts != slots:
+        raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
     if scales is not None and scales.shape != (adapters,):
         raise ValueError(f"scales must be [{adapters}], not {tuple(scales.shape)}")
     held = ((slots,), (adapters, experts)) if experts else ((slots,),)  # flattened, by adapter and expert
@@ -462,12 +475,12 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
 
 
 def lora(x, a, b, adapter_ids, scales=None, base=None, y=None, expert_ids=None,
-         x_row_per_pair: bool = False, workspace=None, stream=None):
+         x_row_per_pair: bool = False, workspace=None, stream=None, experts=None):
     """y [rows, n] = base + scales[id] * B_id (A_id x) with each row's own
     adapter, via qmm_lora (one problem; see lora_batched).  base None: the
     adapters' part alone; base = y: added in place."""
     return lora_batched([(x, a, b, base, y)], adapter_ids, scales, expert_ids, x_row_per_pair, workspace,
-                        stream)[0]
+                        stream, experts)[0]
 
 
 def convert_bf16(w_bf16, out=None, stream=None):

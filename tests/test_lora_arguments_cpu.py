@@ -122,7 +122,7 @@ def test_weights_laid_out_otherwise():
         ((x, a, h(2, 3, 1, 10, 8), IDS), kw),
         ((x, h(2, 8, 64), h(2, 1, 10, 8), IDS), {}),
         ((x, h(2, 8, 64), h(2, 0, 10, 8), IDS), {}),
-        ((x, flat_a, h(3, 2, 10, 8), IDS), dict(kw, scales=scales)),
+        ((x, flat_a, h(3, 2, 10, 8), IDS), dict(kw, scales=scales, experts=3)),
     ]:
         with pytest.raises(ValueError, match="problem 0: a .* and b .* must be"):
             qmm.lora(*args, **other)
@@ -135,3 +135,32 @@ def test_weights_laid_out_otherwise():
                         ((x, flat_a, b, IDS), dict(kw, scales=scales))]:
         with pytest.raises(ValueError, match="device tensor"):
             qmm.lora(*args, **other)
+
+
+def test_the_number_of_experts_of_flattened_weights():
+    """Flattened weights do not say how many experts they are of: the call can,
+    and scales of another length are then refused; so do weights of another
+    problem that are not flattened.  Otherwise scales [adapters] say it."""
+    x, a, b = h(4, 64), h(12, 8, 64), h(12, 10, 8)
+    kw = dict(expert_ids=EXPERT_IDS)
+    for scales in (torch.ones(6), torch.ones(2), torch.ones(12), torch.ones(5)):
+        with pytest.raises(ValueError, match=r"scales must be \[4\]"):
+            qmm.lora(x, a, b, IDS, scales=scales, experts=3, **kw)
+        with pytest.raises(ValueError, match=r"scales must be \[4\]"):
+            qmm.lora(x, a, b.view(4, 3, 10, 8), IDS, scales=scales, **kw)
+        with pytest.raises(ValueError, match=r"scales must be \[4\]"):
+            qmm.lora_batched([(x, a, b, None, None), (x, a.view(4, 3, 8, 64), b, None, None)], IDS, scales, EXPERT_IDS)
+    for scales in (None, torch.ones(4)):
+        with pytest.raises(ValueError, match="device tensor"):
+            qmm.lora(x, a, b, IDS, scales=scales, experts=3, **kw)
+    with pytest.raises(ValueError, match="device tensor"):
+        qmm.lora(x, a, b, IDS, scales=torch.ones(6), **kw)
+    with pytest.raises(ValueError, match="12 sets of weights are not a multiple of 5 experts"):
+        qmm.lora(x, a, b, IDS, experts=5, **kw)
+    with pytest.raises(ValueError, match="problem 0: a .* and b .* must be"):
+        qmm.lora(x, a.view(4, 3, 8, 64), b, IDS, experts=4, **kw)
+    with pytest.raises(ValueError, match="experts=3 without expert_ids"):
+        qmm.lora(x, a, b, IDS, experts=3)
+    for wrong in (0, -3):
+        with pytest.raises(ValueError, match="experts="):
+            qmm.lora(x, a, b, IDS, experts=wrong, **kw)
