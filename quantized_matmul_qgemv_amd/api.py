@@ -393,12 +393,10 @@ def _lora_rows(problems, adapter_ids, expert_ids):
 
 
 def _lora_experts(problems, slots, scales, expert_ids, experts):
-    """The number of experts of a call (0 without expert_ids): as given, of
-    weights that are not flattened, or by the number of scales."""
+    """The number of experts of a call: as given, of weights that are not
+    flattened, or by the number of scales."""
     if expert_ids is None:
-        if experts is not None:
-            raise ValueError(f"experts={experts} without expert_ids")
-        return 0
+        raise ValueError(f"experts={experts} without expert_ids")
     if experts is not None:
         if experts < 1:
             raise ValueError(f"experts={experts} must be positive")
@@ -435,23 +433,29 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
     `experts` says how many (without it scales do, by being [adapters]: give
     it to have their length checked).  Returns the list of y."""
     t, top_k, slots = _lora_rows(problems, adapter_ids, expert_ids)
-    experts = _lora_experts(problems, slots, scales, expert_ids, experts)
-    adapters = slots // max(1, experts)
-    if experts and adapters * experts != slots:
-        raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
+    if expert_ids is None and experts is None:
+        experts, adapters = 0, slots
+    else:
+        experts = _lora_experts(problems, slots, scales, expert_ids, experts)
+        adapters = slots // max(1, experts)
+        if experts and adapters * experts != slots:
+            raise ValueError(f"{slots} sets of weights are not a multiple of {experts} experts")
     if scales is not None and scales.shape != (adapters,):
         raise ValueError(f"scales must be [{adapters}], not {tuple(scales.shape)}")
     held = ((slots,), (adapters, experts)) if experts else ((slots,),)  # flattened, by adapter and expert
+    sizes = []
     for i, (_, a, b, _, _) in enumerate(problems):
-        if a.shape[:-2] not in held or b.shape[:-2] not in held or b.shape[-1] != a.shape[-2]:
-            raise ValueError(f"problem {i}: a {tuple(a.shape)} and b {tuple(b.shape)} must be [{slots}, rank, k] "
+        sa, sb = a.shape, b.shape
+        flat = len(sa) == 3 and len(sb) == 3 and sa[0] == slots and sb[0] == slots
+        if not (flat or (sa[:-2] in held and sb[:-2] in held)) or sb[-1] != sa[-2]:
+            raise ValueError(f"problem {i}: a {tuple(sa)} and b {tuple(sb)} must be [{slots}, rank, k] "
                              f"and [{slots}, n, rank]" + (f", or [{adapters}, {experts}, ...]" if experts else ""))
+        sizes.append((sb[-2], sa[-1], sa[-2]))
     rows, per_pair = t * top_k, 1 if x_row_per_pair else 0
     x_rows = rows if per_pair else t
     d, checked, out = None, [], []
     for i, (x, a, b, base, y) in enumerate(problems):
-        rank, k = a.shape[-2:]
-        n = b.shape[-2]
+        n, k, rank = sizes[i]
         if x.shape != (x_rows, k):
             raise ValueError(f"problem {i}: x must be [{x_rows}, {k}], not {tuple(x.shape)}")
         if base is not None and base.shape != (rows, n):
