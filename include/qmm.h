@@ -323,14 +323,15 @@ int qmm_moe_combine(const float* y_pairs, const float* weights, float* y, int t,
  *       group_keep groups of the largest scores stay
  *   expert_ids[t, :] = the top_k experts of those groups by c, largest first
  *   weights[t, j] = scale * s[id_j] / (renormalize ? sum_j s[id_j] : 1)
- * Equal values go to the lower index, of groups and of experts.  The choice is
- * that of exact arithmetic: logits are compared as they are where only the
- * order of the scores counts (no bias, group_top = 1), and s and c are
- * formed in 64 bits otherwise.  The bias moves the choice, never the weights.
+ * Equal values go to the lower index, of groups and of experts.  Where only the
+ * order of the scores counts (no bias, group_top = 1) logits are compared as
+ * they are; otherwise the choice is that of the formulas in 64 bits (where
+ * sigmoid scores of logits from 37 on are 1 and equal).  The bias moves the
+ * choice, never the weights, which are formed in 64 bits and rounded once.
  * A logit of -inf is an expert switched off: its score is 0 (it can still be
  * returned, with weight 0, where top_k experts cannot be had otherwise or a
- * bias lifts it).  A renormalizing sum of 0 (every chosen expert switched
- * off) gives weights 0.  A token whose scores, choices or group scores hold
+ * bias lifts it).  A renormalizing sum of 0 (every chosen expert switched off,
+ * or of a sigmoid logit below -745, 0 in 64 bits) gives weights 0.  A token whose scores, choices or group scores hold
  * a NaN (a NaN logit or bias; +inf under softmax) gets expert_ids
  * 0 .. top_k-1 and NaN weights, so that the failure shows in its output.
  *   groups: divides E, at most 64 (1: no groups, then group_keep = 1);
@@ -371,8 +372,9 @@ int qmm_moe_topk(const float* logits, const float* bias, int32_t* expert_ids, fl
  * (two adapters on one output are two calls).  Adapters of smaller
  * rank are padded with zeros to the problem's rank, a multiple of 8 up to
  * 256; k is a multiple of 64 up to 2^24, adapters x experts at most 4096, n at most
- * 2097152, t * top_k at most 2^27.  A B x is held in fp32 throughout (products of fp16, A x exact to
- * 2^-23 of the row's largest value); non-finite adapter weights make
+ * 2097152, t * top_k at most 2^27.  Both products are sums of exact fp16 products in fp32; on the
+ * matrix cores the sum A x enters the second one as two fp16, off by up to 2^-23
+ * of the row's largest value of it.  Non-finite adapter weights make
  * non-finite outputs.  Results do not depend on scheduling, nor on what the
  * other rows hold.
  * Workspace: qmm_lora_workspace_size bytes for `rows` = t * top_k and `slots` =

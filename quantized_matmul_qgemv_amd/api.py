@@ -425,7 +425,8 @@ def lora_batched(problems, adapter_ids, scales=None, expert_ids=None, x_row_per_
                  workspace=None, stream=None, experts=None):
     """y = base + scales[id] * B_id (A_id x) for the projections of one input
     (q, k and v; gate and up) in the same launches, via qmm_lora: a list of
-    (x, a, b, base, y) with base None, or y itself to add in place.
+    (x, a, b, base, y) with base None, or y itself to add in place; no y may
+    overlap an x, or the base or y of another problem.
     adapter_ids int32 [T], -1 for no adapter; a [adapters, rank, k] and
     b [adapters, n, rank] fp16.  With expert_ids [T, top_k] the rows are the
     pairs of a routed layer and each adapter has weights for every expert:

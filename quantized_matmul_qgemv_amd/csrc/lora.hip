@@ -279,7 +279,10 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink64_kernel(LoraArgs g)
 // against 80 us for 16384 x 2560, rank 64).  base and y pass once and are
 // larger than the caches where it matters: non-temporal, 35 against 41 us
 // for 2048 x 9728, rank 16 (4.6 TB/s); in place, or between a producer and a
-// consumer of y, within 4 % either way.  RC: ranks in steps of 32.
+// consumer of y, within 4 % either way.  Where n is no multiple of 4, or y or
+// base not on 16 bytes, single columns are loaded and stored one after the
+// other (base may be y): whole calls of 2048 x 2560 x 9729 65 us against 45 of
+// 9728, 16384 x 4096 x 2561 of rank 64 216 against 108.  RC: ranks in steps of 32.
 template <int BM, int RC>
 struct Columns {
   static constexpr int CT = BM / 16;
@@ -918,8 +921,21 @@ static long lora_tiles(int rows, int tile_rows, int slots) {
 //     pairs on 512 slots): 28.5 / 33.7 (rank 16, 768, 2048), 53.2 / 57.5
 //     (rank 64, 768, 2048: A of 96 KB), 36.4 / 37.2 (rank 32, 2048, 768),
 //     58.5 / 58.2 (rank 64, 2048, 768: 256 KB).  Hence A up to 128 KB.
-//   sorted rows, tiles of 64 where they are filled and there are enough of
-//     them to fill the chip; [hi | lo] of a rank over 128 outgrows LDS there.
+//   two launches on the matrix cores, tiles found by ballots against sorted
+//     rows (2560, 4096): 8 rows of rank 128 12.1 / 14.8 on one slot and 11.7 /
+//     15.0 on 8, 64 rows on 64 slots 29.8 / 33.6; 256 rows on 256 slots of rank
+//     64 51.2 / 51.7, of rank 128 99.8 / 101.1.  Rows that share slots are sorted
+//     faster from 32 on: 32 rows of rank 128 on one slot 16.6 / 15.6, 256 on 8
+//     of rank 64 29.7 / 16.7, on one 47.3 / 16.7.  Hence ballots up to
+//     kLoraDirectRows (a thread for each row), which is late for such calls.
+//   sorted rows, tiles of 16 against tiles of 64 (2560, 4096): rank 64 with 24
+//     rows a slot, 2048 rows 48.0 / 42.2 and 8192 rows 156.5 / 133.1; with 20,
+//     48.4 / 47.3 and 176.6 / 149.8; with 12, 52.8 / 60.5 and 203.8 / 201.5.
+//     Rank 128 with 24, 2048 rows 62.4 / 66.1; with 12, 80.3 / 111.7.  Hence 24
+//     rows a slot.  520 rows on one slot, rank 64 19.8 / 22.5, rank 128 25.8 /
+//     27.7, rank 16 22.3 / 18.1; 1000 rows on 10 slots 26.9 / 24.1, 38.6 / 32.4
+//     and 26.5 / 19.1.  Hence 1024 rows, which is late for small ranks.
+//     [hi | lo] of a rank over 128 outgrows LDS in tiles of 64.
 size_t lora_layout(LoraArgs& g) {
   int rank = 0;
   long a_bytes = 0;  // the largest A of a slot

@@ -12,9 +12,11 @@
 //
 // Without a bias and with groups judged by their best expert the scores only
 // enter through their order, and both scores increase with the logit: the
-// choice then compares the logits themselves and is exact.  Otherwise s and c
-// are formed in 64 bits, so that the choice is that of the formulas to 1e-15
-// whatever the logits.  The weights are formed in 64 bits and rounded once.
+// choice then compares the logits themselves and is exact.  Otherwise the
+// choice is that of s and c in 64 bits, whatever the logits: formed so where a
+// token has a whole wave; where it has sixteen lanes formed in fp32 first, and
+// again in 64 bits where fp32 cannot tell two choices apart.  The weights are
+// formed in 64 bits and rounded once.
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(kTopkWaves * 64) void moe_topk_wave_kernel(TopkArgs
 // compared, 700 by logit), small calls by latency.  Against a whole wave
 // per token in 64 bits: 1 x 128 top-8 2.7 / 9.9 us, 2048 x 128 3.9 / 12.8,
 // 32768 x 256 by logit 12.9, by sigmoid and bias 16.3, in 8 groups 21 / 147
-// (1.7 TB/s of logits).  Sixteen lanes, as a row's exchanges are single DPP
+// (1.6 TB/s of logits).  Sixteen lanes, as a row's exchanges are single DPP
 // moves and four tokens share every instruction.
 constexpr int kRowTokens = 16;  // tokens per workgroup of 256
 constexpr float kNear = 0x1p-19f;
