@@ -83,7 +83,7 @@ int check_plan_size(const char* fn, size_t plan_bytes, int t, int top_k, int e) 
 // Rows of one adapter call: tiles of 16, 256 threads each, within 2^32 threads.
 constexpr long kMaxLoraRows = 1 << 27;
 constexpr int kMaxLoraK = 1 << 24;
-constexpr int kMaxLoraN = 1 << 21;  // ranges of 256 columns and more, of all problems in one grid dimension
+constexpr int kMaxLoraN = 1 << 21;  // ranges of 256 columns or more in one grid dimension
 
 bool lora_k(int k) { return k >= 64 && k % 64 == 0 && k <= kMaxLoraK; }
 bool lora_rank(int rank) { return rank >= 8 && rank % 8 == 0 && rank <= qmm::kLoraMaxRank; }
