@@ -150,11 +150,12 @@ def _run_routed(s, c):
     import quantized_matmul_qgemv_amd as qmm
     if s["workspace"] is None:
         s["workspace"] = qmm.i8_grouped_workspace(s["x"])
-    kw = {"a_scales": s["x_scales"], "workspace": s["workspace"]}
     if c["op"] == "swiglu":
-        return qmm.i8_moe_gate_up_swiglu(*s["weights"], s["x"], s["ids"], s["plan"], h=s["y"], **kw)
+        return qmm.i8_moe_gate_up_swiglu(*s["weights"], s["x"], s["ids"], s["plan"], x_scales=s["x_scales"], h=s["y"],
+                                         workspace=s["workspace"])
     w, ws = s["weights"][0]
-    return qmm.i8_gemm_grouped(w, ws, s["x"], s["ids"], s["plan"], a_row_per_pair=True, y=s["y"], **kw)
+    return qmm.i8_gemm_grouped(w, ws, s["x"], s["ids"], s["plan"], a_row_per_pair=True, a_scales=s["x_scales"], y=s["y"],
+                               workspace=s["workspace"])
 
 
 def _plain_rows(s):
