@@ -401,6 +401,89 @@ int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter
              const int32_t* expert_ids, const float* scales, int t, int top_k, int adapters,
              int experts, void* workspace, size_t workspace_bytes, qmm_stream stream);
 
+/* -------------------------------------------------- products in 8-bit integers
+ * Both operands are 8-bit integers with one fp32 scale a row: w [n, k] a scale
+ * for each output channel, x [m, k] a scale for each token.
+ *   s[r]    = fp32( max_k |x[r, k]| / 127 )
+ *   q[r, k] = rint( x[r, k] / s[r] )     (the exact quotient, ties to even)
+ *   y[m, n] = s_x[m] s_w[n] sum_k q_x[m, k] q_w[n, k]  (+ bias[n])
+ * qmm_i8_quantize gives codes and scales of rows: of a weight matrix at load
+ * time (a row is an output channel), of activations (a row is a token).  The
+ * products also take x in 16 or 32 bits and round its rows themselves, to the
+ * same codes.  The sum is an exact int32; it is rounded to fp32, multiplied by
+ * the two scales and rounded after each (then once more to a 16-bit y), so a
+ * result depends on nothing but its own row, column and scales.
+ * A row whose largest magnitude is below 2^-119 has scale 0 and codes 0; a row
+ * that holds a NaN or an infinity has scale NaN and codes 0, and so a row of
+ * NaN in y.  Given codes may be anything from -128 to 127.
+ *   types  QMM_F32, QMM_F16, QMM_BF16 (bit patterns); QMM_I8: codes, with their scales
+ *   sizes  k a multiple of 16 up to 131008; n in [1, 2097152]; m in [0, 16777215];
+ *          together the outputs of a call at most 2^35
+ *   w, x, codes and workspaces 16-byte aligned, scales and bias 4-byte, y by
+ *   its type (on 16 bytes, with n a multiple of 4, it is stored by whole pieces)
+ * Errors of all: INVALID_ARG, UNSUPPORTED (type), WORKSPACE, HIP. */
+#define QMM_F32 0
+#define QMM_F16 1
+#define QMM_BF16 2
+#define QMM_I8 3
+
+/* codes [m, k], scales [m] of x [m, k] (x_type: QMM_F32, QMM_F16 or QMM_BF16).
+ * One launch; codes and scales must not overlap x or each other. */
+int qmm_i8_quantize(const void* x, int x_type, int8_t* codes, float* scales, int m, int k,
+                    qmm_stream stream);
+
+/* Up to 8 products of one call (q, k and v; gate and up; or one alone) run
+ * together.  Problems that name the same x (with the same m, k and type) have it
+ * rounded once.  No y may overlap another problem's y, or any operand.
+ *   x_scales  [m] with x_type QMM_I8, NULL otherwise
+ *   bias      [n] fp32 or NULL
+ * Workspace: qmm_i8_gemm_workspace_size bytes (x, m, n, k and x_type of the
+ * problems are read; 0 for sizes that are refused, and where none is needed:
+ * then it may be NULL), contents on entry do not matter; calls (and captured
+ * graphs) that share one must not run concurrently.  m = 0: the problem does
+ * nothing.  One to three launches, by sizes and types. */
+typedef struct {
+  const int8_t* w;
+  const float* w_scales;
+  const void* x;
+  const float* x_scales;
+  const float* bias;
+  void* y;
+  int32_t m;
+  int32_t n;
+  int32_t k;
+  int32_t x_type;
+  int32_t y_type;
+} qmm_i8_problem;
+
+size_t qmm_i8_gemm_workspace_size(const qmm_i8_problem* problems, int count);
+int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size_t workspace_bytes,
+                qmm_stream stream);
+
+/* The experts' products of a routed layer, from a plan of qmm_moe_route for the
+ * same (t, top_k, e): pairs, rows and out-of-range experts (NaN rows) as in
+ * qmm_qgemm_grouped_routed; a plan built for other counts makes the whole
+ * output NaN.
+ *   qmm_i8_gemm_grouped  y[p, :] = the product of row(p) of a with w [E, n, k] of
+ *       the pair's expert, w_scales [E, n]; y [t * top_k, n] of y_type
+ *   qmm_i8_moe_gate_up_swiglu  h[p, :] = silu(g) u with g and u the products of
+ *       x's row p / top_k with w_gate and w_up [E, n, k] of the pair's expert
+ *       (fp32 until h, of h_type, is rounded)
+ *   a, x  of a_type / x_type; with QMM_I8 its scales, one for each row, NULL
+ *         otherwise.  rows * k must be below 2^32.
+ * Workspace: qmm_i8_grouped_workspace_size bytes for the rows of a or x (0 with
+ * QMM_I8: then it may be NULL), as above. */
+size_t qmm_i8_grouped_workspace_size(int rows, int k, int x_type);
+int qmm_i8_gemm_grouped(const int8_t* w, const float* w_scales, const void* a, const float* a_scales,
+                        int a_type, int a_row_per_pair, const void* plan, size_t plan_bytes, void* y,
+                        int y_type, int t, int top_k, int e, int n, int k, void* workspace,
+                        size_t workspace_bytes, qmm_stream stream);
+int qmm_i8_moe_gate_up_swiglu(const int8_t* w_gate, const float* s_gate, const int8_t* w_up,
+                              const float* s_up, const void* x, const float* x_scales, int x_type,
+                              const void* plan, size_t plan_bytes, void* h, int h_type, int t, int top_k,
+                              int e, int n, int k, void* workspace, size_t workspace_bytes,
+                              qmm_stream stream);
+
 /* ------------------------------------------------ load-time quantization
  * Asymmetric min/max quantization of a dense fp32 weight W[n, k] into the
  * packed format above: per group, s = fp16((max - min) / L) and

@@ -22,6 +22,7 @@ QMM_ERR_HIP = 4
 QMM_WEIGHTS_TILED = 0x100  # bits flag: weights from qmm_repack_tiled
 QMM_SCALES_TILED = 0x200  # bits flag: scales from qmm_repack_scales_tiled (biases unused)
 QMM_SCORE_SOFTMAX, QMM_SCORE_SIGMOID = 0, 1  # scores of qmm_moe_topk
+QMM_F32, QMM_F16, QMM_BF16, QMM_I8 = 0, 1, 2, 3  # types of the products in 8-bit integers
 QMM_GROUPED_SCRATCH_BYTES = 1 << 20  # static scratch of qmm_qgemm_grouped_noalloc
 
 STATUS_NAMES = {0: "QMM_OK", 1: "QMM_ERR_INVALID_ARG", 2: "QMM_ERR_UNSUPPORTED",
@@ -51,6 +52,12 @@ class LoraProblem(C.Structure):
                 ("x_row_per_pair", C.c_int32)]
 
 
+class I8Problem(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("w_scales", C.c_void_p), ("x", C.c_void_p), ("x_scales", C.c_void_p),
+                ("bias", C.c_void_p), ("y", C.c_void_p), ("m", C.c_int32), ("n", C.c_int32),
+                ("k", C.c_int32), ("x_type", C.c_int32), ("y_type", C.c_int32)]
+
+
 P, I, SZ, F = C.c_void_p, C.c_int, C.c_size_t, C.c_float
 
 SIGNATURES = {
@@ -75,6 +82,12 @@ SIGNATURES = {
     "qmm_moe_topk": (I, [P, P, P, P, I, I, I, I, I, I, I, I, F, P]),
     "qmm_lora_workspace_size": (SZ, [C.POINTER(LoraProblem), I, I, I]),
     "qmm_lora": (I, [C.POINTER(LoraProblem), I, P, P, P, I, I, I, I, P, SZ, P]),
+    "qmm_i8_quantize": (I, [P, I, P, P, I, I, P]),
+    "qmm_i8_gemm_workspace_size": (SZ, [C.POINTER(I8Problem), I]),
+    "qmm_i8_gemm": (I, [C.POINTER(I8Problem), I, P, SZ, P]),
+    "qmm_i8_grouped_workspace_size": (SZ, [I, I, I]),
+    "qmm_i8_gemm_grouped": (I, [P, P, P, P, I, I, P, SZ, P, I, I, I, I, I, I, P, SZ, P]),
+    "qmm_i8_moe_gate_up_swiglu": (I, [P, P, P, P, P, P, I, P, SZ, P, I, I, I, I, I, I, P, SZ, P]),
     "qmm_convert_bf16": (I, [P, P, SZ, P]),
     "qmm_repack_tiled": (I, [P, P, I, I, I, P]),
     "qmm_repack_scales_tiled": (I, [P, P, P, I, I, P]),

@@ -16,7 +16,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import GemmProblem, GemvProblem, LoraProblem, check, lib
+from ._lib import GemmProblem, GemvProblem, I8Problem, LoraProblem, check, lib
 
 GROUP = 64
 
@@ -486,6 +486,158 @@ def lora(x, a, b, adapter_ids, scales=None, base=None, y=None, expert_ids=None,
     adapters' part alone; base = y: added in place."""
     return lora_batched([(x, a, b, base, y)], adapter_ids, scales, expert_ids, x_row_per_pair, workspace,
                         stream, experts)[0]
+
+
+_TYPES = {torch.float32: _lib.QMM_F32, torch.float16: _lib.QMM_F16, torch.bfloat16: _lib.QMM_BF16,
+          torch.int8: _lib.QMM_I8}
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+_ROWS = _FLOATS + (torch.int8,)
+_C = (torch.int8,)
+
+
+def i8_quantize(x, codes=None, scales=None, stream=None):
+    """(codes int8 [m, k], scales fp32 [m]) of the rows of x [m, k] (fp32, fp16 or
+    bf16), via qmm_i8_quantize: scale = max |x| / 127, code = the whole number
+    nearest to x / scale.  Of weights [n, k] at load time (a row is an output
+    channel; stacked experts [E, n, k] give [E, n, k] and [E, n]), of activations
+    (a row is a token)."""
+    if x.dim() < 2:
+        raise ValueError(f"x must be [m, k], not {tuple(x.shape)}")
+    k = x.shape[-1]
+    if codes is None:
+        codes = _empty(x.shape, torch.int8, x.device, stream)
+    elif codes.shape != x.shape:
+        raise ValueError(f"codes must be {list(x.shape)}, not {tuple(codes.shape)}")
+    if scales is None:
+        scales = _empty(x.shape[:-1], torch.float32, x.device, stream)
+    elif scales.shape != x.shape[:-1]:
+        raise ValueError(f"scales must be {list(x.shape[:-1])}, not {tuple(scales.shape)}")
+    d = _device_of(x, "x")
+    check(lib().qmm_i8_quantize(_ptr(x, "x", _FLOATS, d), _TYPES[x.dtype], _ptr(codes, "codes", _C, d),
+                                _ptr(scales, "scales", _Y, d), scales.numel(), k, _stream_on(stream, d)))
+    return codes, scales
+
+
+def i8_gemm_workspace(problems, stream=None):
+    """A workspace for i8_gemm and i8_gemm_batched calls of these problems (kept
+    by the caller; calls that share one must not overlap in time)."""
+    arr = (I8Problem * len(problems))()
+    for i, (w, _, x, _, _, _) in enumerate(problems):
+        if x.dtype not in _TYPES:
+            raise TypeError(f"problem {i}: x has dtype {x.dtype}, expected one of {_ROWS}")
+        arr[i] = I8Problem(None, None, x.data_ptr(), None, None, None, x.shape[0], w.shape[0], x.shape[1],
+                           _TYPES[x.dtype], 0)
+    need = lib().qmm_i8_gemm_workspace_size(arr, len(problems))
+    return _empty(max(need, 16), torch.uint8, problems[0][2].device, stream)
+
+
+def i8_gemm_batched(problems, dtype=torch.float32, workspace=None, stream=None):
+    """y [m, n] = x_scales w_scales (x w^T) + bias for several products in the same
+    launches (q, k and v; gate and up), via qmm_i8_gemm: a list of
+    (w int8 [n, k], w_scales fp32 [n], x [m, k], x_scales, bias, y).  x int8 codes
+    with x_scales fp32 [m], or fp32, fp16 or bf16 with None (its rows are rounded
+    as by i8_quantize; once for problems that name the same x); bias fp32 [n] or
+    None; y fp32, fp16 or bf16, or None for one of `dtype`.  Returns the list of y."""
+    if not problems:
+        raise ValueError("no problems")
+    d, checked, out = None, [], []
+    for i, (w, ws, x, xs, bias, y) in enumerate(problems):
+        if x.dim() != 2 or w.dim() != 2 or w.shape[1] != x.shape[1]:
+            raise ValueError(f"problem {i}: w {tuple(w.shape)} and x {tuple(x.shape)} must be [n, k] and [m, k]")
+        m, k = x.shape
+        n = w.shape[0]
+        if ws.shape != (n,):
+            raise ValueError(f"problem {i}: w_scales must be [{n}], not {tuple(ws.shape)}")
+        if xs is not None and xs.shape != (m,):
+            raise ValueError(f"problem {i}: x_scales must be [{m}], not {tuple(xs.shape)}")
+        if bias is not None and bias.shape != (n,):
+            raise ValueError(f"problem {i}: bias must be [{n}], not {tuple(bias.shape)}")
+        if y is None:
+            y = _empty((m, n), dtype, x.device, stream)
+        elif y.shape != (m, n):
+            raise ValueError(f"problem {i}: y must be [{m}, {n}], not {tuple(y.shape)}")
+        if d is None:
+            d = _device_of(x, "x")
+        checked.append(I8Problem(_ptr(w, "w", _C, d), _ptr(ws, "w_scales", _Y, d), _ptr(x, "x", _ROWS, d),
+                                 _ptr(xs, "x_scales", _Y, d), _ptr(bias, "bias", _Y, d), _ptr(y, "y", _FLOATS, d),
+                                 m, n, k, _TYPES[x.dtype], _TYPES[y.dtype]))
+        out.append(y)
+    arr = (I8Problem * len(checked))(*checked)
+    if workspace is None:
+        need = lib().qmm_i8_gemm_workspace_size(arr, len(checked))
+        workspace = _empty(need, torch.uint8, out[0].device, stream) if need else None
+    check(lib().qmm_i8_gemm(arr, len(checked), _ptr(workspace, "workspace", (torch.uint8,), d),
+                            0 if workspace is None else workspace.numel(), _stream_on(stream, d)))
+    return out
+
+
+def i8_gemm(w, w_scales, x, x_scales=None, bias=None, y=None, dtype=torch.float32, workspace=None, stream=None):
+    """y [m, n] = x_scales w_scales (x w^T) + bias of 8-bit codes (one problem; see
+    i8_gemm_batched)."""
+    return i8_gemm_batched([(w, w_scales, x, x_scales, bias, y)], dtype, workspace, stream)[0]
+
+
+def i8_grouped_workspace(x, stream=None):
+    """A workspace for i8_gemm_grouped and i8_moe_gate_up_swiglu calls on rows like
+    x's (kept by the caller; calls that share one must not overlap in time)."""
+    if x.dtype not in _TYPES:
+        raise TypeError(f"x has dtype {x.dtype}, expected one of {_ROWS}")
+    need = lib().qmm_i8_grouped_workspace_size(x.shape[0], x.shape[1], _TYPES[x.dtype])
+    return _empty(max(need, 16), torch.uint8, x.device, stream)
+
+
+def _i8_routed(weights, x, x_scales, expert_ids, plan, per_pair, y, dtype, workspace, stream):
+    """The checks that both routed products share; returns what their calls take."""
+    if expert_ids.dim() != 2:
+        raise ValueError(f"expert_ids must be [T, top_k], not {tuple(expert_ids.shape)}")
+    t, top_k = expert_ids.shape
+    w = weights[0][0]
+    if w.dim() != 3 or x.dim() != 2 or w.shape[2] != x.shape[1]:
+        raise ValueError(f"w {tuple(w.shape)} and the rows {tuple(x.shape)} must be [E, n, k] and [rows, k]")
+    e, n, k = w.shape
+    for v, vs in weights:
+        if v.shape != (e, n, k) or vs.shape != (e, n):
+            raise ValueError(f"weights {tuple(v.shape)} and their scales {tuple(vs.shape)} must be [{e}, {n}, {k}] and [{e}, {n}]")
+    rows = t * top_k if per_pair else t
+    if x.shape[0] != rows:
+        raise ValueError(f"there must be {rows} rows, not {x.shape[0]}")
+    if x_scales is not None and x_scales.shape != (rows,):
+        raise ValueError(f"the rows' scales must be [{rows}], not {tuple(x_scales.shape)}")
+    if y is None:
+        y = _empty((t * top_k, n), dtype, x.device, stream)
+    elif y.shape != (t * top_k, n):
+        raise ValueError(f"the output must be [{t * top_k}, {n}], not {tuple(y.shape)}")
+    d = _device_of(x, "x")
+    px = _ptr(x, "x", _ROWS, d)
+    if workspace is None and x.dtype != torch.int8:
+        workspace = i8_grouped_workspace(x, stream)
+    head = [p for v, vs in weights for p in (_ptr(v, "w", _C, d), _ptr(vs, "w_scales", _Y, d))]
+    head += [px, _ptr(x_scales, "scales", _Y, d), _TYPES[x.dtype]]
+    tail = [_ptr(plan, "plan", (torch.uint8,), d), plan.numel(), _ptr(y, "y", _FLOATS, d), _TYPES[y.dtype], t, top_k, e,
+            n, k, _ptr(workspace, "workspace", (torch.uint8,), d), 0 if workspace is None else workspace.numel(),
+            _stream_on(stream, d)]
+    return head, tail, y
+
+
+def i8_gemm_grouped(w, w_scales, a, expert_ids, plan, a_row_per_pair: bool, a_scales=None, y=None,
+                    dtype=torch.float32, workspace=None, stream=None):
+    """y [T*top_k, n]: each pair's row of a with its expert's weights, both as 8-bit
+    codes, via qmm_i8_gemm_grouped.  w int8 [E, n, k], w_scales fp32 [E, n]; a int8
+    codes with a_scales, or fp32, fp16 or bf16, [T, k] or with a_row_per_pair
+    [T*top_k, k]; plan from moe_route on the same expert_ids [T, top_k]."""
+    head, tail, y = _i8_routed([(w, w_scales)], a, a_scales, expert_ids, plan, a_row_per_pair, y, dtype, workspace, stream)
+    check(lib().qmm_i8_gemm_grouped(*head, 1 if a_row_per_pair else 0, *tail))
+    return y
+
+
+def i8_moe_gate_up_swiglu(gate, up, x, expert_ids, plan, x_scales=None, h=None, dtype=torch.float16, workspace=None,
+                          stream=None):
+    """h [T*top_k, n] = silu(x W_gate^T) * (x W_up^T) per pair, weights and rows as
+    8-bit codes, via qmm_i8_moe_gate_up_swiglu; gate and up are (int8 [E, n, k],
+    fp32 [E, n]), x and plan as for i8_gemm_grouped."""
+    head, tail, h = _i8_routed([gate, up], x, x_scales, expert_ids, plan, False, h, dtype, workspace, stream)
+    check(lib().qmm_i8_moe_gate_up_swiglu(*head, *tail))
+    return h
 
 
 def convert_bf16(w_bf16, out=None, stream=None):

@@ -124,6 +124,42 @@ int check_lora_overlaps(const char* fn, const qmm_lora_problem* problems, int co
   return QMM_OK;
 }
 
+// Products in 8-bit integers.
+constexpr int kMaxI8Rows = (1 << 24) - 1;
+constexpr int kMaxI8N = 1 << 21;
+constexpr double kMaxI8Outputs = 34359738368.0;  // 2^35: the tiles' threads stay below 2^32
+
+size_t i8_width(int type) { return type == QMM_I8 ? 1 : type == QMM_F32 ? 4 : 2; }
+bool i8_k(int k) { return k >= 16 && k % 16 == 0 && k <= qmm::kI8MaxK; }
+bool i8_x_type(int type) { return type >= QMM_F32 && type <= QMM_I8; }
+bool i8_y_type(int type) { return type >= QMM_F32 && type <= QMM_BF16; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+size_t i8_codes_bytes(size_t rows, size_t k) { return up256(rows * k) + up256(rows * 4); }
+
+int check_i8_sizes(const char* fn, int n, int k) {
+  if (n < 1 || n > kMaxI8N) return fail(QMM_ERR_INVALID_ARG, "%s: n=%d must be in [1, %d]", fn, n, kMaxI8N);
+  if (!i8_k(k))
+    return fail(QMM_ERR_INVALID_ARG, "%s: k=%d must be a positive multiple of 16 up to %d", fn, k, qmm::kI8MaxK);
+  return QMM_OK;
+}
+
+int check_i8_types(const char* fn, int x_type, int y_type) {
+  if (!i8_x_type(x_type)) return fail(QMM_ERR_UNSUPPORTED, "%s: type %d of x is none of QMM_F32, QMM_F16, QMM_BF16, QMM_I8", fn, x_type);
+  if (!i8_y_type(y_type)) return fail(QMM_ERR_UNSUPPORTED, "%s: type %d of the output is none of QMM_F32, QMM_F16, QMM_BF16", fn, y_type);
+  return QMM_OK;
+}
+
+bool i8_same_x(const qmm_i8_problem& a, const qmm_i8_problem& b) {
+  return a.x == b.x && a.x_type == b.x_type && a.m == b.m && a.k == b.k;
+}
+
+// The problem before i whose x is that of i, or i itself.
+int i8_first_of(const qmm_i8_problem* problems, int i) {
+  for (int j = 0; j < i; ++j)
+    if (i8_same_x(problems[j], problems[i])) return j;
+  return i;
+}
+
 }  // namespace
 
 extern "C" {
@@ -729,6 +765,193 @@ int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter
   g.v = static_cast<float*>(workspace);
   g.plan = static_cast<int32_t*>(workspace);
   return hip_status(qmm::launch_lora(g, (hipStream_t)stream), fn);
+}
+
+int qmm_i8_quantize(const void* x, int x_type, int8_t* codes, float* scales, int m, int k,
+                    qmm_stream stream) {
+  const char* fn = "qmm_i8_quantize";
+  clear_error();
+  if (x_type == QMM_I8 || !i8_x_type(x_type))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: type %d of x is none of QMM_F32, QMM_F16, QMM_BF16", fn, x_type);
+  if (m < 0 || m > kMaxI8Rows) return fail(QMM_ERR_INVALID_ARG, "%s: m=%d must be in [0, %d]", fn, m, kMaxI8Rows);
+  if (int st = check_i8_sizes(fn, 1, k)) return st;
+  if (m == 0) return QMM_OK;
+  CHECK_PTR(x, 16);
+  CHECK_PTR(codes, 16);
+  CHECK_PTR(scales, 4);
+  const size_t values = (size_t)m * k, x_bytes = values * i8_width(x_type);
+  if (overlap(codes, values, x, x_bytes) || overlap(scales, (size_t)m * 4, x, x_bytes) ||
+      overlap(codes, values, scales, (size_t)m * 4))
+    return fail(QMM_ERR_INVALID_ARG, "%s: x, codes and scales overlap", fn);
+  qmm::I8QuantizeArgs q{};
+  q.job[0] = qmm::I8QuantizeJob{x, codes, scales, m, k, x_type, 0};
+  q.count = 1;
+  return hip_status(qmm::launch_i8_quantize(q, (hipStream_t)stream), fn);
+}
+
+size_t qmm_i8_gemm_workspace_size(const qmm_i8_problem* problems, int count) {
+  if (problems == nullptr || count < 1 || count > qmm::kI8MaxProblems) return 0;
+  size_t need = 0;
+  for (int i = 0; i < count; ++i) {
+    const qmm_i8_problem& q = problems[i];
+    if (q.m < 0 || q.m > kMaxI8Rows || q.n < 1 || q.n > kMaxI8N || !i8_k(q.k) || !i8_x_type(q.x_type)) return 0;
+    if (q.x_type != QMM_I8 && i8_first_of(problems, i) == i) need += i8_codes_bytes(q.m, q.k);
+  }
+  return need;
+}
+
+int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size_t workspace_bytes,
+                qmm_stream stream) {
+  const char* fn = "qmm_i8_gemm";
+  clear_error();
+  if (problems == nullptr) return fail(QMM_ERR_INVALID_ARG, "%s: null problems", fn);
+  if (count < 1 || count > qmm::kI8MaxProblems)
+    return fail(QMM_ERR_INVALID_ARG, "%s: count=%d must be in [1, %d]", fn, count, qmm::kI8MaxProblems);
+  double outputs = 0;
+  for (int i = 0; i < count; ++i) {
+    const qmm_i8_problem& q = problems[i];
+    if (q.m < 0 || q.m > kMaxI8Rows)
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: m=%d must be in [0, %d]", fn, i, q.m, kMaxI8Rows);
+    if (int st = check_i8_sizes(fn, q.n, q.k)) return st;
+    if (int st = check_i8_types(fn, q.x_type, q.y_type)) return st;
+    outputs += (double)q.m * q.n;
+    if (q.m == 0) continue;
+    if (!q.w || !q.w_scales || !q.x || !q.y)
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d has a null pointer", fn, i);
+    if ((q.x_type == QMM_I8) != (q.x_scales != nullptr))
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: x_scales belong to an x of type QMM_I8, and only there", fn, i);
+    if (!aligned(q.w, 16) || !aligned(q.x, 16))
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: w or x is not 16-byte aligned", fn, i);
+    if (!aligned(q.w_scales, 4) || !aligned(q.x_scales, 4) || !aligned(q.bias, 4))
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: scales or bias are not 4-byte aligned", fn, i);
+    if (!aligned(q.y, i8_width(q.y_type)))
+      return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: y is not %zu-byte aligned", fn, i, i8_width(q.y_type));
+  }
+  if (outputs > kMaxI8Outputs) return fail(QMM_ERR_INVALID_ARG, "%s: too many outputs", fn);
+  for (int i = 0; i < count; ++i) {  // the problems run together: no y on what another one reads or writes
+    const qmm_i8_problem& p = problems[i];
+    if (p.m == 0) continue;
+    const size_t y_bytes = (size_t)p.m * p.n * i8_width(p.y_type);
+    for (int j = 0; j < count; ++j) {
+      const qmm_i8_problem& q = problems[j];
+      if (q.m == 0) continue;
+      const char* what = nullptr;
+      if (j < i && overlap(p.y, y_bytes, q.y, (size_t)q.m * q.n * i8_width(q.y_type))) what = "y";
+      else if (overlap(p.y, y_bytes, q.x, (size_t)q.m * q.k * i8_width(q.x_type))) what = "x";
+      else if (overlap(p.y, y_bytes, q.w, (size_t)q.n * q.k)) what = "w";
+      else if (overlap(p.y, y_bytes, q.w_scales, (size_t)q.n * 4) ||
+               (q.x_scales && overlap(p.y, y_bytes, q.x_scales, (size_t)q.m * 4))) what = "scales";
+      else if (q.bias && overlap(p.y, y_bytes, q.bias, (size_t)q.n * 4)) what = "bias";
+      if (what) return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: y overlaps the %s of problem %d", fn, i, what, j);
+    }
+  }
+  const size_t need = qmm_i8_gemm_workspace_size(problems, count);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
+    CHECK_PTR(workspace, 16);
+  }
+  qmm::I8QuantizeArgs qa{};
+  qmm::I8GemmArgs g{};
+  char* next = static_cast<char*>(workspace);
+  int at[qmm::kI8MaxProblems];  // of a problem's codes: its place in qa
+  for (int i = 0; i < count; ++i) {
+    const qmm_i8_problem& q = problems[i];
+    if (q.m == 0) continue;
+    qmm::I8Problem& p = g.p[g.count++];
+    p = qmm::I8Problem{static_cast<const int8_t*>(q.x), q.x_scales, q.w, q.w_scales, q.bias, q.y, q.m, q.n, q.k, q.y_type, 0};
+    if (q.x_type == QMM_I8) continue;
+    const int from = i8_first_of(problems, i);
+    if (from == i) {
+      at[i] = qa.count;
+      qa.job[qa.count++] = qmm::I8QuantizeJob{q.x, reinterpret_cast<int8_t*>(next),
+                                              reinterpret_cast<float*>(next + up256((size_t)q.m * q.k)), q.m, q.k, q.x_type, 0};
+      next += i8_codes_bytes(q.m, q.k);
+    }
+    p.x = qa.job[at[from]].codes;
+    p.sx = qa.job[at[from]].scales;
+  }
+  if (g.count == 0) return QMM_OK;
+  if (qa.count > 0)
+    if (int st = hip_status(qmm::launch_i8_quantize(qa, (hipStream_t)stream), fn)) return st;
+  return hip_status(qmm::launch_i8_gemm(g, (hipStream_t)stream), fn);
+}
+
+size_t qmm_i8_grouped_workspace_size(int rows, int k, int x_type) {
+  if (rows < 0 || rows > kMaxI8Rows || !i8_k(k) || !i8_x_type(x_type) || x_type == QMM_I8) return 0;
+  return i8_codes_bytes(rows, k);
+}
+
+static int i8_routed(const char* fn, const int8_t* w, const float* w_scales, const int8_t* w2, const float* w2_scales,
+                     bool gated, const void* x, const float* x_scales, int x_type, int per_pair, const void* plan,
+                     size_t plan_bytes, void* y, int y_type, int t, int top_k, int e, int n, int k, void* workspace,
+                     size_t workspace_bytes, qmm_stream stream) {
+  clear_error();
+  if (t < 0) return fail(QMM_ERR_INVALID_ARG, "%s: t=%d must be >= 0", fn, t);
+  if (top_k < 1) return fail(QMM_ERR_INVALID_ARG, "%s: top_k=%d must be >= 1", fn, top_k);
+  if (e < 1 || e > kMaxExperts) return fail(QMM_ERR_INVALID_ARG, "%s: e=%d must be in [1, %d]", fn, e, kMaxExperts);
+  if (per_pair != 0 && per_pair != 1) return fail(QMM_ERR_INVALID_ARG, "%s: a_row_per_pair must be 0 or 1", fn);
+  if (int st = check_i8_sizes(fn, n, k)) return st;
+  if (int st = check_i8_types(fn, x_type, y_type)) return st;
+  const long pairs = (long)t * top_k;
+  if (pairs > kMaxI8Rows) return fail(QMM_ERR_INVALID_ARG, "%s: too many pairs", fn);
+  const int rows = per_pair ? (int)pairs : t;
+  if ((unsigned long)rows * k > 0xFFFFFFFFul)
+    return fail(QMM_ERR_INVALID_ARG, "%s: %d rows of k=%d: rows * k must be below 2^32", fn, rows, k);
+  if ((double)pairs * n > kMaxI8Outputs) return fail(QMM_ERR_INVALID_ARG, "%s: too many outputs", fn);
+  if (t == 0) return QMM_OK;
+  CHECK_PTR(w, 16);
+  CHECK_PTR(w_scales, 4);
+  if (gated) {
+    CHECK_PTR(w2, 16);
+    CHECK_PTR(w2_scales, 4);
+  }
+  CHECK_PTR(x, 16);
+  if (x_type == QMM_I8) CHECK_PTR(x_scales, 4);
+  else if (x_scales != nullptr)
+    return fail(QMM_ERR_INVALID_ARG, "%s: scales belong to rows of type QMM_I8, and only there", fn);
+  CHECK_PTR(plan, 16);
+  CHECK_PTR(y, i8_width(y_type));
+  if (int st = check_plan_size(fn, plan_bytes, t, top_k, e)) return st;
+  const size_t need = qmm_i8_grouped_workspace_size(rows, k, x_type);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
+    CHECK_PTR(workspace, 16);
+  }
+  const size_t y_bytes = (size_t)pairs * n * i8_width(y_type);
+  if (overlap(y, y_bytes, x, (size_t)rows * k * i8_width(x_type)))
+    return fail(QMM_ERR_INVALID_ARG, "%s: the output overlaps its rows", fn);
+  qmm::I8MoeArgs g{static_cast<const int8_t*>(x), x_scales, w, w_scales, w2, w2_scales, static_cast<const int32_t*>(plan),
+                   y, t, top_k, e, n, k, per_pair, y_type, qmm::moe_plan_rows((int)pairs, e), 1};
+  if (x_type != QMM_I8) {
+    qmm::I8QuantizeArgs qa{};
+    int8_t* codes = static_cast<int8_t*>(workspace);
+    float* scales = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)rows * k));
+    qa.job[0] = qmm::I8QuantizeJob{x, codes, scales, rows, k, x_type, 0};
+    qa.count = 1;
+    if (int st = hip_status(qmm::launch_i8_quantize(qa, (hipStream_t)stream), fn)) return st;
+    g.x = codes;
+    g.sx = scales;
+  }
+  return hip_status(qmm::launch_i8_moe(g, (hipStream_t)stream), fn);
+}
+
+int qmm_i8_gemm_grouped(const int8_t* w, const float* w_scales, const void* a, const float* a_scales,
+                        int a_type, int a_row_per_pair, const void* plan, size_t plan_bytes, void* y,
+                        int y_type, int t, int top_k, int e, int n, int k, void* workspace,
+                        size_t workspace_bytes, qmm_stream stream) {
+  return i8_routed("qmm_i8_gemm_grouped", w, w_scales, nullptr, nullptr, false, a, a_scales, a_type, a_row_per_pair, plan,
+                   plan_bytes, y, y_type, t, top_k, e, n, k, workspace, workspace_bytes, stream);
+}
+
+int qmm_i8_moe_gate_up_swiglu(const int8_t* w_gate, const float* s_gate, const int8_t* w_up,
+                              const float* s_up, const void* x, const float* x_scales, int x_type,
+                              const void* plan, size_t plan_bytes, void* h, int h_type, int t, int top_k,
+                              int e, int n, int k, void* workspace, size_t workspace_bytes,
+                              qmm_stream stream) {
+  return i8_routed("qmm_i8_moe_gate_up_swiglu", w_gate, s_gate, w_up, s_up, true, x, x_scales, x_type, 0, plan, plan_bytes,
+                   h, h_type, t, top_k, e, n, k, workspace, workspace_bytes, stream);
 }
 
 int qmm_quantize(const float* w_f32, uint32_t* words, uint16_t* scales, uint16_t* biases,

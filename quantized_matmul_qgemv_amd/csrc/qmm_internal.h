@@ -160,6 +160,7 @@ constexpr size_t kGroupedScratchBytes = 1u << 20;
 hipError_t grouped_scratch(void** ptr);
 // bucket = false: ws already holds a routing plan for these ids (launch_moe_route).
 hipError_t launch_qgemm_grouped(const GroupedArgs& a, int bits, void* ws, bool bucket, hipStream_t st);
+int moe_plan_rows(int pairs, int experts);  // row tile of a routing plan
 hipError_t launch_moe_route(const int32_t* ids, int t, int top_k, int e, void* plan, hipStream_t st);
 hipError_t launch_moe_swiglu(const uint32_t* wg, const uint16_t* sg, const uint16_t* bg,
                              const uint32_t* wu, const uint16_t* su, const uint16_t* bu,
@@ -222,6 +223,53 @@ struct LoraArgs {
 };
 size_t lora_layout(LoraArgs& g);
 hipError_t launch_lora(const LoraArgs& g, hipStream_t st);
+
+// Products in 8-bit integers (i8_gemm.hip, i8_moe.hip).
+constexpr int kI8MaxProblems = 8;
+constexpr int kI8MaxK = 131008;  // 128 * 128 * k stays below 2^31
+struct I8QuantizeJob {
+  const void* x;
+  int8_t* codes;
+  float* scales;
+  int32_t m, k, type;
+  int32_t first;  // workgroup
+};
+struct I8QuantizeArgs {
+  I8QuantizeJob job[kI8MaxProblems];
+  int32_t count;
+};
+hipError_t launch_i8_quantize(I8QuantizeArgs& g, hipStream_t st);
+
+struct I8Problem {
+  const int8_t* x;
+  const float* sx;
+  const int8_t* w;
+  const float* sw;
+  const float* bias;
+  void* y;
+  int32_t m, n, k, y_type;
+  int32_t first;  // workgroup
+};
+struct I8GemmArgs {
+  I8Problem p[kI8MaxProblems];
+  int32_t count;
+};
+hipError_t launch_i8_gemm(I8GemmArgs& g, hipStream_t st);
+
+struct I8MoeArgs {
+  const int8_t* x;
+  const float* sx;
+  const int8_t* w;
+  const float* sw;
+  const int8_t* w2;  // up, or null
+  const float* sw2;
+  const int32_t* plan;
+  void* y;
+  int32_t t, top_k, e, n, k, a_row_per_pair, y_type;
+  int32_t plan_rows;  // row tile of the plan
+  int32_t subs;       // workgroups that share one of its row tiles
+};
+hipError_t launch_i8_moe(I8MoeArgs& g, hipStream_t st);
 
 hipError_t launch_quantize(const float* w, uint32_t* words, uint16_t* s, uint16_t* b, int n,
                            int k, int bits, int group_size, hipStream_t st);

@@ -1,0 +1,220 @@
+"""Products in 8-bit integers against their formulas in 64 bits: every type, at
+sizes with ragged edges, rows of zeros, infinities and NaN."""
+import numpy as np
+import pytest
+
+import i8_testlib as ref
+from qmm_testlib import Guarded, dev, say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import quantized_matmul_qgemv_amd as qmm  # noqa: E402
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+FLOATS = [F32, F16, BF16]
+ids = lambda v: str(v).split(".")[-1] if isinstance(v, torch.dtype) else None  # noqa: E731
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def activations(r, m, k, dtype):
+    """Rows of very different size, as a device tensor of the type."""
+    x = r.standard_normal((m, k)) * np.exp(r.standard_normal((m, 1)))
+    return torch.from_numpy(x).to(dtype).cuda()
+
+
+def weights(r, n, k):
+    """Codes over the whole range, -128 among them, and scales."""
+    return r.integers(-128, 128, (n, k)).astype(np.int8), (r.random(n) * 1e-3 + 1e-5).astype(np.float32)
+
+
+# ------------------------------------------------------------------ rounding
+
+@pytest.mark.parametrize("dtype", FLOATS, ids=ids)
+@pytest.mark.parametrize("m,k", [(1, 16), (3, 48), (5, 1008), (4, 1024), (7, 1040), (2, 4096), (3, 4112),
+                                 (2, 16384), (2, 16400), (1, 131008), (1000, 768), (257, 2560)])
+def test_codes_are_those_of_the_exact_quotient(dtype, m, k):
+    say("i8 quantize", dtype, m, k)
+    r = np.random.default_rng([1, m, k])
+    x = activations(r, m, k, dtype)
+    codes, scales = Guarded((m, k), torch.int8), Guarded((m,), F32)
+    qmm.i8_quantize(x, codes.t, scales.t)
+    torch.cuda.synchronize()
+    codes.check("codes")
+    scales.check("scales")
+    q, s = ref.rows_f64(f64(x))
+    assert np.array_equal(scales.t.cpu().numpy(), s)
+    assert np.array_equal(codes.t.cpu().numpy(), q)
+
+
+@pytest.mark.parametrize("dtype", FLOATS, ids=ids)
+def test_codes_at_and_beside_every_half(dtype):
+    """Rows whose scale makes many quotients exact halves, and their neighbours in
+    the type: 127 a, (n + 1/2) a and one step to each side."""
+    r = np.random.default_rng(2)
+    rows = []
+    for e in range(-8, 9):
+        for a in (1.0, 1.25, 1.0 + 2.0 ** -7, 1.5 - 2.0 ** -6):
+            x = torch.tensor([(n + 0.5) * a * 2.0 ** e for n in range(-127, 127)] + [127.0 * a * 2.0 ** e] * 2,
+                             dtype=torch.float64).to(dtype)
+            bits = torch.int32 if dtype == F32 else torch.int16
+            near = torch.cat([(x.view(bits) + d).view(dtype) for d in (-1, 0, 1)])
+            near = torch.where(near.abs() > x[-1].abs(), x[-1], near)
+            rows.append(torch.cat([near, x[-1:].repeat(768 - near.numel() % 768)])[:768])
+    x = torch.stack(rows)[torch.from_numpy(r.permutation(len(rows)))].cuda()
+    say("i8 quantize halves", dtype, tuple(x.shape))
+    codes, scales = qmm.i8_quantize(x)
+    q, s = ref.rows_f64(f64(x))
+    assert np.array_equal(scales.cpu().numpy(), s)
+    assert np.array_equal(codes.cpu().numpy(), q)
+
+
+@pytest.mark.parametrize("dtype", FLOATS, ids=ids)
+@pytest.mark.parametrize("k", [16, 1040, 4112])
+def test_rows_of_zeros_tiny_huge_and_not_finite(dtype, k):
+    say("i8 quantize edges", dtype, k)
+    big = float(torch.finfo(dtype).max)
+    rows = [np.zeros(k)] + [np.full(k, v) for v in (big, -big, 1e-5, 2.0 ** -24)]
+    if dtype != F16:
+        rows += [np.full(k, v) for v in (2.0 ** -119, 2.0 ** -119 * (1 - 2.0 ** -8), 1e-38, 1e-40)]
+    for bad in (np.nan, np.inf, -np.inf):
+        for at in (0, k // 2, k - 1):
+            x = np.linspace(-1, 1, k)
+            x[at] = bad
+            rows.append(x)
+    x = torch.from_numpy(np.stack(rows)).to(dtype).cuda()
+    codes, scales = qmm.i8_quantize(x)
+    q, s = ref.rows_f64(f64(x))
+    assert np.array_equal(scales.cpu().numpy(), s, equal_nan=True)
+    assert np.array_equal(codes.cpu().numpy(), q)
+
+
+def test_stacked_rows_and_no_rows():
+    r = np.random.default_rng(4)
+    x = torch.from_numpy(r.standard_normal((3, 5, 64)).astype(np.float32)).cuda()
+    codes, scales = qmm.i8_quantize(x)
+    q, s = ref.rows_f64(f64(x))
+    assert np.array_equal(codes.cpu().numpy(), q) and np.array_equal(scales.cpu().numpy(), s)
+    codes, scales = qmm.i8_quantize(x[:0])
+    assert codes.shape == (0, 5, 64) and scales.shape == (0, 5)
+
+
+# ------------------------------------------------------------------ products
+
+SIZES = [(1, 1, 16), (1, 7, 48), (1, 1000, 2560), (2, 33, 64), (3, 64, 112), (4, 129, 128), (5, 31, 144),
+         (8, 100, 4112), (15, 65, 240), (16, 256, 1088), (17, 257, 1040), (31, 2, 656), (33, 96, 384),
+         (48, 515, 272), (64, 64, 2576), (65, 130, 400), (100, 1001, 208), (128, 128, 1024), (129, 387, 528),
+         (200, 1, 4096), (255, 255, 80), (256, 512, 640), (257, 260, 1296), (300, 2049, 96), (513, 770, 352),
+         (1030, 129, 176), (1, 40, 131008), (70, 4, 32)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_products_of_codes(m, n, k):
+    say("i8 gemm codes", m, n, k)
+    r = np.random.default_rng([5, m, n, k])
+    w, ws = weights(r, n, k)
+    q = r.integers(-128, 128, (m, k)).astype(np.int8)
+    s = (r.random(m) * 0.1).astype(np.float32)
+    y = Guarded((m, n), F32)
+    qmm.i8_gemm(dev(w), dev(ws), dev(q), dev(s), y=y.t)
+    torch.cuda.synchronize()
+    y.check("y")
+    ref.check(f64(y.t), ref.product_f64(q, s, w, ws), F32, (m, n, k))
+
+
+@pytest.mark.parametrize("xt,yt", [(F32, F32), (F16, F32), (BF16, BF16), (F16, F16), (F32, BF16), (BF16, F16)], ids=ids)
+@pytest.mark.parametrize("m,n,k,bias", [(1, 515, 2560, True), (3, 64, 1040, False), (16, 130, 4112, True),
+                                        (40, 1000, 256, True), (130, 257, 1088, False), (300, 384, 768, True)])
+def test_products_of_activations(xt, yt, m, n, k, bias):
+    say("i8 gemm", xt, yt, m, n, k)
+    r = np.random.default_rng([6, m, n, k])
+    w, ws = weights(r, n, k)
+    b = r.standard_normal(n).astype(np.float32) if bias else None
+    x = activations(r, m, k, xt)
+    y = Guarded((m, n), yt)
+    qmm.i8_gemm(dev(w), dev(ws), x, bias=None if b is None else dev(b), y=y.t)
+    torch.cuda.synchronize()
+    y.check("y")
+    ref.check(f64(y.t), ref.product_f64(*ref.rows_f64(f64(x)), w, ws, b), yt, (m, n, k))
+
+
+@pytest.mark.parametrize("m", [1, 5, 16, 60, 300])
+def test_given_codes_and_codes_formed_in_the_call_agree_bit_by_bit(m):
+    say("i8 gemm both ways", m)
+    r = np.random.default_rng([7, m])
+    w, ws = weights(r, 333, 1040)
+    x = activations(r, m, 1040, F16)
+    q, s = qmm.i8_quantize(x)
+    a = qmm.i8_gemm(dev(w), dev(ws), x)
+    b = qmm.i8_gemm(dev(w), dev(ws), q, s)
+    assert torch.equal(a, b)
+    # and a row alone is the row among others
+    assert torch.equal(qmm.i8_gemm(dev(w), dev(ws), x[:1].contiguous()), a[:1])
+
+
+@pytest.mark.parametrize("m", [1, 7, 33, 300])
+def test_largest_sums_are_exact(m):
+    """All codes at -128 over the longest k: 128 * 128 * 131008 is below 2^31."""
+    say("i8 gemm largest sums", m)
+    k, n = 131008, 5
+    w = torch.full((n, k), -128, dtype=torch.int8, device="cuda")
+    x = torch.full((m, k), -128, dtype=torch.int8, device="cuda")
+    x[:, 1::2] = 127
+    x[0] = -128
+    one = torch.ones(max(m, n), device="cuda")
+    y = qmm.i8_gemm(w, one[:n].contiguous(), x, one[:m].contiguous())
+    want = np.full((m, n), -128.0 * (127 - 128) * k / 2)
+    want[0] = 128.0 * 128 * k
+    assert np.array_equal(f64(y), np.float32(want).astype(np.float64))
+
+
+def test_rows_that_are_not_finite_stay_their_own():
+    say("i8 gemm not finite")
+    r = np.random.default_rng(8)
+    for m in (3, 40, 300):
+        w, ws = weights(r, 70, 208)
+        x = activations(r, m, 208, F16)
+        clean = qmm.i8_gemm(dev(w), dev(ws), x)
+        x[1, 5], x[m - 1, 207] = float("inf"), float("nan")
+        y = qmm.i8_gemm(dev(w), dev(ws), x)
+        assert y[1].isnan().all() and y[m - 1].isnan().all()
+        keep = [i for i in range(m) if i not in (1, m - 1)]
+        assert torch.equal(y[keep], clean[keep])
+
+
+def test_several_products_of_one_call():
+    say("i8 gemm batched")
+    r = np.random.default_rng(9)
+    for m in (1, 20, 200):
+        x, x2 = activations(r, m, 1088, BF16), activations(r, m + 3, 96, F32)
+        q, s = qmm.i8_quantize(x)
+        problems, wants = [], []
+        for i, (n, xi, si, yt) in enumerate([(300, x, None, F32), (65, x, None, F16), (1, q, s, BF16), (129, x2, None, F32)]):
+            w, ws = weights(r, n, xi.shape[1])
+            b = r.standard_normal(n).astype(np.float32) if i % 2 else None
+            y = Guarded((xi.shape[0], n), yt)
+            problems.append((dev(w), dev(ws), xi, si, None if b is None else dev(b), y))
+            wants.append((ref.product_f64(*(ref.rows_f64(f64(xi)) if si is None else (f64(q), f64(s))), w, ws, b), yt))
+        given = [p[:5] + (p[5].t,) for p in problems]
+        ws_ = qmm.i8_gemm_workspace(given)
+        ws_.fill_(0xFF)
+        out = qmm.i8_gemm_batched(given, workspace=ws_)
+        torch.cuda.synchronize()
+        for i, (p, y, (want, yt)) in enumerate(zip(problems, out, wants)):
+            p[5].check(i)
+            ref.check(f64(y), want, yt, (m, i))
+
+
+def test_no_rows_and_empty_problems_beside_others():
+    r = np.random.default_rng(10)
+    w, ws = weights(r, 9, 64)
+    x = activations(r, 4, 64, F16)
+    assert qmm.i8_gemm(dev(w), dev(ws), x[:0]).shape == (0, 9)
+    a, b = qmm.i8_gemm_batched([(dev(w), dev(ws), x[:0], None, None, None), (dev(w), dev(ws), x, None, None, None)])
+    assert a.shape == (0, 9) and torch.equal(b, qmm.i8_gemm(dev(w), dev(ws), x))
