@@ -26,9 +26,6 @@ namespace qmm {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kI8Step = 128;  // bytes of k a step
-constexpr int kI8Pieces = kI8Step / 16;
-
 // A buffer descriptor of all that follows `base` (the same in every lane):
 // every access of the tile is inside its operand by construction.
 __device__ __forceinline__ i32x4 i8_rows(const void* base) {
@@ -50,116 +47,166 @@ __device__ __forceinline__ void i8_copy(uint32_t lds, i32x4 base, uint32_t voff,
                : "memory");
 }
 
-// All but this wave's last N copies have landed, its LDS reads are back, and
-// the other waves' likewise.
+// All but this wave's last N copies have landed.
 template <int N>
-__device__ __forceinline__ void i8_join() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+__device__ __forceinline__ void i8_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
+
+// This wave's LDS reads are back, and the other waves are here too.
+__device__ __forceinline__ void i8_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
-// BM rows of X by BN rows of W on WM x WN waves, a ring of ST stages.
-template <int BM_, int BN_, int WM_, int WN_, int ST_>
+// BM rows of X by BN rows of W on WM x WN waves, a ring of ST stages of BK bytes
+// of k.
+template <int BM_, int BN_, int WM_, int WN_, int ST_, int BK_>
 struct I8Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, BK = BK_;
   static constexpr int WAVES = WM * WN;
   static constexpr int THREADS = 64 * WAVES;
   static constexpr int TM = BM / WM / 32;  // blocks of 32 x 32 a wave
   static constexpr int TN = BN / WN / 32;
-  static constexpr int CA = BM / 8 / WAVES;  // copies a wave and step: 8 rows each
-  static constexpr int CB = BN / 8 / WAVES;
-  static constexpr int STAGE = (BM + BN) * kI8Step;
+  static constexpr int PIECES = BK / 16;       // of 16 bytes, of a row
+  static constexpr int RC = 64 / PIECES;       // rows a copy
+  static constexpr int CX = BM / RC;           // copies a step: X's, then W's,
+  static constexpr int CW = BN / RC;
+  static constexpr int COPIES = CX + CW;
+  static constexpr int EACH = (COPIES + WAVES - 1) / WAVES;  // dealt to the waves in turn
+  static constexpr int SHORT = COPIES % WAVES;               // waves from here on have one less (0: none)
+  static constexpr int STAGE = (BM + BN) * BK;
   static constexpr int LDS = ST * STAGE;
+  static_assert(BK == 64 || BK == 128, "half a line or a line");
   static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "whole blocks");
-  static_assert(WAVES % 2 == 0 && BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "whole copies");
-  static_assert((ST - 2) * (CA + CB) <= 63 && ST >= 2, "vmcnt counts to 63");
+  static_assert(BM % RC == 0 && BN % (2 * RC) == 0 && WAVES % 2 == 0 && CX % WAVES == 0, "whole copies");
+  static_assert((ST - 1) * EACH <= 63 && ST >= 2, "vmcnt counts to 63");
 };
+
+// Where piece c of row r stands in its row of a stage: XOR with this.
+template <class S>
+__device__ __forceinline__ int i8_key(int r) {
+  return S::BK == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
 
 // One tile.  x_row(i) is the row of x at `xbase` that stands in row i of the
 // tile, w_row(i) likewise (any valid row where the tile reaches past the
 // operand: what it gives is not stored); steps [s0, s1) of k.
 // acc[i][j]: block of X rows i, W rows j of the wave; lane l, register r hold
 // the product of W row 8 (r / 4) + 4 (l / 32) + r % 4 and X row l % 32.
-// GATED: the tile's BN rows of W are BN / 2 at `wbase` and as many at `wbase2`,
-// and of a wave's TN blocks the first half is the former's.
+// GATED: of each 32 of the tile's BN rows of W 16 are at `wbase` (gate) and the
+// same 16 at `wbase2` (up), so that both products of an output stand in one
+// lane, eight registers apart.
 template <class S, bool GATED, class XRow, class WRow>
 __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const int8_t* wbase, const int8_t* wbase2,
                                         WRow w_row, int k, int s0, int s1, char* lds, i32x16 (&acc)[S::TM][S::TN]) {
-  static_assert(!GATED || (S::TN % 2 == 0 && S::CB % 2 == 0), "halves of whole blocks and copies");
+  // 16 rows are 2 copies (of 8 rows) or one: which base a copy has is its wave's alone
+  static_assert(!GATED || (S::RC == 8 && S::WAVES % 4 == 0), "a wave's copies are all gate's or all up's");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
-  const i32x4 xr = i8_rows(xbase), wr = i8_rows(wbase), wr2 = i8_rows(wbase2);
-  // the copies: 8 rows each, of which this lane takes one piece
-  const uint32_t piece = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
-  uint32_t xo[S::CA], wo[S::CB];
+  const i32x4 xr = i8_rows(xbase), wr = i8_rows(GATED && (wave & 2) ? wbase2 : wbase);
+  // the copies: RC rows each, of which this lane takes one piece (its key is the
+  // same in all: they are an even number of waves apart)
+  const int mine = lane / S::PIECES;
+  const int piece = (lane % S::PIECES) ^ i8_key<S>(wave * S::RC + mine);
+  uint32_t from[S::EACH];
 #pragma unroll
-  for (int j = 0; j < S::CA; ++j) xo[j] = (uint32_t)x_row((j * S::WAVES + wave) * 8 + (lane >> 3)) * (uint32_t)k + piece * 16;
-#pragma unroll
-  for (int j = 0; j < S::CB; ++j) {
-    const int i = (j * S::WAVES + wave) * 8 + (lane >> 3);
-    wo[j] = (uint32_t)w_row(GATED && j >= S::CB / 2 ? i - S::BN / 2 : i) * (uint32_t)k + piece * 16;
+  for (int j = 0; j < S::EACH; ++j) {
+    int i = (j * S::WAVES + wave) * S::RC + mine;
+    if (j * S::WAVES < S::CX) {
+      i = x_row(i);
+    } else {
+      i = i - S::BM < S::BN ? i - S::BM : S::BN - 1;
+      i = w_row(GATED ? i / 32 * 16 + i % 16 : i);
+    }
+    from[j] = (uint32_t)i * (uint32_t)k + piece * 16;
   }
   const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_address(lds));
   // past the end of k the last step reads the row's last piece again; the
   // operands of X are set to zero there
-  const int whole = k / kI8Step;            // steps that are whole
-  const int pieces = (k % kI8Step) / 16;    // pieces of the step behind them
-  const uint32_t back = (int)piece >= pieces ? (piece - (pieces - 1)) * 16 : 0;
+  const int whole = k / S::BK;            // steps that are whole
+  const int pieces = (k % S::BK) / 16;    // pieces of the step behind them
+  const uint32_t back = piece >= pieces ? (piece - (pieces - 1)) * 16 : 0;
+  const bool less = S::SHORT != 0 && wave >= S::SHORT;
 
   auto copy = [&](int step, int stage) {
     const uint32_t at = ring + stage * S::STAGE + wave * 1024;
-    const uint32_t less = step < whole ? 0 : back;
-    const uint32_t soff = (uint32_t)step * kI8Step;
+    const uint32_t off = step < whole ? 0 : back;
+    const uint32_t soff = (uint32_t)step * S::BK;
 #pragma unroll
-    for (int j = 0; j < S::CA; ++j) i8_copy(at + j * S::WAVES * 1024, xr, xo[j] - less, soff);
-#pragma unroll
-    for (int j = 0; j < S::CB; ++j) i8_copy(at + S::BM * kI8Step + j * S::WAVES * 1024, GATED && j >= S::CB / 2 ? wr2 : wr, wo[j] - less, soff);
-  };
-
-  const int r = lane & 31, h = lane >> 5;
-  const int key = (r >> 1) & 7;
-  const char* xs = lds + (wm * S::TM * 32 + r) * kI8Step;
-  constexpr int TC = GATED ? S::TN / 2 : S::TN;
-  const char* ws = lds + (S::BM + wn * TC * 32 + r) * kI8Step;
-  auto multiply = [&](int stage, auto masked, int valid) {
-    const int at = stage * S::STAGE;
-#pragma unroll
-    for (int q = 0; q < kI8Step / 32; ++q) {
-      const int o = at + (((2 * q + h) ^ key) << 4);
-      i32x4 a[S::TN], b[S::TM];
-#pragma unroll
-      for (int j = 0; j < S::TN; ++j) a[j] = *reinterpret_cast<const i32x4*>(ws + o + (j < TC ? j * 32 : S::BN / 2 + (j - TC) * 32) * kI8Step);
-#pragma unroll
-      for (int i = 0; i < S::TM; ++i) b[i] = *reinterpret_cast<const i32x4*>(xs + o + i * 32 * kI8Step);
-      if constexpr (decltype(masked)::value) {
-        if (2 * q + h >= valid)
-#pragma unroll
-          for (int i = 0; i < S::TM; ++i) b[i] = i32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < S::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[j], b[i], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < S::EACH; ++j) {
+      if (j == S::EACH - 1 && less) break;
+      i8_copy(at + j * S::WAVES * 1024, j * S::WAVES < S::CX ? xr : wr, from[j] - off, soff);
     }
   };
-  using Plain = std::false_type;
-  using Masked = std::true_type;
+  // all but the copies of the last N steps have landed, in every wave
+  auto join = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (less) i8_wait<N * (S::EACH - 1)>();
+    else i8_wait<N * S::EACH>();
+    i8_meet();
+  };
+  using None = std::integral_constant<int, 0>;
+
+  const int r = lane & 31, h = lane >> 5;
+  const int key = i8_key<S>(r);
+  const char* xs = lds + (wm * S::TM * 32 + r) * S::BK;
+  const char* ws = lds + (S::BM + wn * S::TN * 32 + r) * S::BK;
+  // a step's products of 32 bytes of k; the operands of the next one are read
+  // while one multiplies
+  i32x4 a[2][S::TN], b[2][S::TM];
+  auto read = [&](int stage, int q, i32x4 (&a)[S::TN], i32x4 (&b)[S::TM]) {
+    const int o = stage * S::STAGE + (((2 * q + h) ^ key) << 4);
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) a[j] = *reinterpret_cast<const i32x4*>(ws + o + j * 32 * S::BK);
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) b[i] = *reinterpret_cast<const i32x4*>(xs + o + i * 32 * S::BK);
+  };
+  auto multiply = [&](const i32x4 (&a)[S::TN], const i32x4 (&b)[S::TM]) {
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[j], b[i], acc[i][j], 0, 0, 0);
+  };
+  constexpr int Q = S::BK / 32;
 
 #pragma unroll
-  for (int s = 0; s < S::ST - 1; ++s)
+  for (int s = 0; s < S::ST; ++s)
     if (s0 + s < s1) copy(s0 + s, s);
+  if (s0 + S::ST <= s1) join(std::integral_constant<int, S::ST - 1>{});
+  else join(None{});
+  read(0, 0, a[0], b[0]);
   int stage = 0;
-  for (int s = s0; s < s1; ++s) {
-    if (s + S::ST - 2 < s1) i8_join<(S::ST - 2) * (S::CA + S::CB)>();
-    else i8_join<0>();
-    if (s + S::ST - 1 < s1) copy(s + S::ST - 1, stage == 0 ? S::ST - 1 : stage - 1);
-    if (s < whole) multiply(stage, Plain{}, 0);
-    else multiply(stage, Masked{}, pieces);
+  for (int s = s0; s + 1 < s1; ++s) {
+#pragma unroll
+    for (int q = 0; q < Q - 1; ++q) {
+      read(stage, q + 1, a[(q + 1) & 1], b[(q + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(a[q & 1], b[q & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the stage is read: its place takes the copy of ST steps on, and the next
+    // stage's first operands come while the last product runs
+    if (s + S::ST <= s1) join(std::integral_constant<int, S::ST - 2>{});
+    else join(None{});
+    if (s + S::ST < s1) copy(s + S::ST, stage);
     stage = stage == S::ST - 1 ? 0 : stage + 1;
+    read(stage, 0, a[0], b[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(a[(Q - 1) & 1], b[(Q - 1) & 1]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  const int valid = s1 <= whole ? S::PIECES : pieces;  // of the last step
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (q + 1 < Q) read(stage, q + 1, a[(q + 1) & 1], b[(q + 1) & 1]);
+    if (2 * q + h >= valid)
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i) b[q & 1][i] = i32x4{0, 0, 0, 0};
+    multiply(a[q & 1], b[q & 1]);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -170,35 +217,142 @@ __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const i
 
 enum { kI8F32, kI8F16, kI8BF16, kI8Codes };
 
-__device__ __forceinline__ uint16_t i8_bf16(float v) {  // round to nearest even; NaN stays NaN
-  const uint32_t u = __float_as_uint(v);
-  if (v != v) return (uint16_t)((u >> 16) | 0x40);
-  return (uint16_t)((u + 0x7FFF + ((u >> 16) & 1)) >> 16);
+// Two neighbours in 16 bits, each rounded to nearest even.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t i8_pair(int type, float lo, float hi) {
+  if (type == kI8F16) return as_u32(half2_t{(half_t)lo, (half_t)hi});
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
 }
-
-__device__ __forceinline__ uint16_t i8_f16(float v) { return __builtin_bit_cast(uint16_t, (half_t)v); }
 
 __device__ __forceinline__ float i8_silu(float g) { return g / (1.0f + __expf(-g)); }
 
-// Four neighbouring columns [c, c + 4) of a row, of which `have` exist; wide:
-// the row's address at c takes one store.
-__device__ __forceinline__ void i8_store(void* y, size_t at, int type, const float (&v)[4], int have, bool wide) {
-  if (type == kI8F32) {
-    float* o = static_cast<float*>(y) + at;
-    if (wide && have >= 4) *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-    else
+// The scales of a tile's rows and columns, its bias and where its rows go in y,
+// loaded before the product and used behind it.
+template <class S>
+struct I8Scales {
+  static constexpr int NX = (S::BM + S::THREADS - 1) / S::THREADS, NW = (S::BN + S::THREADS - 1) / S::THREADS;
+  int32_t row[NX];
+  float x[NX], w[NW], b[NW];
+
+  template <class R, class X, class W, class B>
+  __device__ __forceinline__ void load(R y_row, X xs, W ws, B bias) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) if (i < have) o[i] = v[i];
-    return;
+    for (int i = 0; i < NX; ++i) {
+      const int r = threadIdx.x + i * S::THREADS;
+      row[i] = r < S::BM ? y_row(r) : 0;
+      x[i] = r < S::BM ? xs(r, row[i]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int c = threadIdx.x + i * S::THREADS;
+      w[i] = c < S::BN ? ws(c) : 0.0f;
+      b[i] = c < S::BN ? bias(c) : 0.0f;
+    }
   }
-  uint16_t b[4];
+};
+
+constexpr int kI8OutRow = 144;  // bytes of a row of 128 in LDS: neighbours stand 4 banks on
+
+// The tile's results: scaled, rounded, and by way of LDS (32 rows of 128 bytes
+// a wave at a time) out in whole lines, columns [n0, n0 + cols) of n.
+template <class S, bool GATED>
+__device__ __forceinline__ void i8_finish(const i32x16 (&acc)[S::TM][S::TN], const I8Scales<S>& scales, char* lds, void* y,
+                                          int type, bool biased, int n, int n0, int rows, int cols) {
+  constexpr int OC = GATED ? 16 : 32;  // output columns of a block
+  float* xs = reinterpret_cast<float*>(lds);
+  float* ws = xs + S::BM;
+  float* bs = ws + S::BN;
+  int32_t* ys = reinterpret_cast<int32_t*>(bs + S::BN);
+  constexpr int FIRST = (2 * S::BM + 2 * S::BN) * 4;
+  static_assert(FIRST % 16 == 0 && FIRST + S::WAVES * 32 * kI8OutRow <= S::LDS, "fits the ring's place");
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = type == kI8F16 ? i8_f16(v[i]) : i8_bf16(v[i]);
-  uint16_t* o = static_cast<uint16_t*>(y) + at;
-  if (wide && have >= 4) *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
-  else
+  for (int i = 0; i < I8Scales<S>::NX; ++i) {
+    const int r = threadIdx.x + i * S::THREADS;
+    if (r < S::BM) {
+      xs[r] = scales.x[i];
+      ys[r] = scales.row[i];
+    }
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) if (i < have) o[i] = b[i];
+  for (int i = 0; i < I8Scales<S>::NW; ++i) {
+    const int c = threadIdx.x + i * S::THREADS;
+    if (c < S::BN) {
+      ws[c] = scales.w[i];
+      bs[c] = scales.b[i];
+    }
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int r = lane & 31, h = lane >> 5;
+  char* out = lds + FIRST + wave * 32 * kI8OutRow;
+  const int width = type == kI8F32 ? 4 : 2;
+  const int blocks = 128 / (OC * width);  // of OC columns in 128 bytes
+  // whole pieces of 16 bytes where every row starts on one
+  const bool wide = (size_t)n * width % 16 == 0 && ((uintptr_t)y & 15) == 0;
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i) {
+    const int r0 = (wm * S::TM + i) * 32;
+    if (r0 >= rows) break;
+    const float sx = xs[r0 + r];
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) {
+      const int c0 = (wn * S::TN + j) * 32;  // in W's rows
+      const int place = j % blocks;
+#pragma unroll
+      for (int q = 0; q < OC / 8; ++q) {
+        const int c = 8 * q + 4 * h;
+        const float4_t sw = *reinterpret_cast<const float4_t*>(ws + c0 + c);
+        float4_t v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][4 * q + e] * sx * sw[e];
+        if constexpr (GATED) {
+          const float4_t su = *reinterpret_cast<const float4_t*>(ws + c0 + 16 + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = i8_silu(v[e]) * ((float)acc[i][j][4 * q + 8 + e] * sx * su[e]);
+        } else if (biased) {
+          v += *reinterpret_cast<const float4_t*>(bs + c0 + c);
+        }
+        char* o = out + r * kI8OutRow + (place * OC + c) * width;
+        if (type == kI8F32) *reinterpret_cast<float4_t*>(o) = v;
+        else *reinterpret_cast<u32x2*>(o) = u32x2{i8_pair(type, v[0], v[1]), i8_pair(type, v[2], v[3])};
+      }
+      if (place + 1 < blocks && j + 1 < S::TN) continue;
+      // what stands in LDS: columns [s0, s0 + have) of the tile
+      const int s0 = (wn * S::TN + j - place) * OC;
+      const int most = OC * (place + 1);
+      const int have = cols - s0 < most ? cols - s0 : most;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (wide) {
+        const int piece = lane & 7;
+        const int c = piece * (16 / width);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int rr = t * 8 + (lane >> 3);
+          if (r0 + rr < rows && c < have) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(out + rr * kI8OutRow + piece * 16);
+            const size_t at = (size_t)ys[r0 + rr] * n + n0 + s0 + c;
+            *reinterpret_cast<u32x4*>(static_cast<char*>(y) + at * width) = v;
+          }
+        }
+      } else if (type == kI8F32) {
+        for (int t = 0; t < 16; ++t) {
+          const int rr = t * 2 + h;
+          if (r0 + rr < rows && r < have)
+            static_cast<float*>(y)[(size_t)ys[r0 + rr] * n + n0 + s0 + r] = *reinterpret_cast<const float*>(out + rr * kI8OutRow + r * 4);
+        }
+      } else {
+        for (int t = 0; t < 32; ++t)
+          if (r0 + t < rows && lane < have)
+            static_cast<uint16_t*>(y)[(size_t)ys[r0 + t] * n + n0 + s0 + lane] = *reinterpret_cast<const uint16_t*>(out + t * kI8OutRow + lane * 2);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
 }
 
 }  // namespace qmm

@@ -167,15 +167,22 @@ hipError_t launch_i8_quantize(I8QuantizeArgs& g, hipStream_t st) {
 
 // ----------------------------------------------------------------- products
 
+constexpr int kI8Band = 8;
+
 template <class S>
 __global__ __launch_bounds__(S::THREADS) void i8_gemm_kernel(I8GemmArgs g) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
-  int b = blockIdx.x, which = 0;
+  // workgroups are dealt to the 8 XCDs in turn: each XCD gets a run of tiles
+  const int each = gridDim.x / 8, more = gridDim.x % 8, xcd = blockIdx.x % 8;
+  int b = xcd * each + (xcd < more ? xcd : more) + blockIdx.x / 8, which = 0;
   while (which + 1 < g.count && b >= g.p[which + 1].first) ++which;
   const I8Problem& p = g.p[which];
   b -= p.first;
-  const int tiles_m = (p.m + S::BM - 1) / S::BM;
-  const int tm = b % tiles_m, tn = b / tiles_m;
+  const int tiles_m = (p.m + S::BM - 1) / S::BM, tiles_n = (p.n + S::BN - 1) / S::BN;
+  // bands of kI8Band row tiles, down each column of a band
+  const int band = b / (kI8Band * tiles_n), in = b - band * kI8Band * tiles_n;
+  const int high = tiles_m - band * kI8Band < kI8Band ? tiles_m - band * kI8Band : kI8Band;
+  const int tm = band * kI8Band + in % high, tn = in / high;
   const int m0 = tm * S::BM, n0 = tn * S::BN;
   const int rows = p.m - m0 < S::BM ? p.m - m0 : S::BM;
   const int cols = p.n - n0 < S::BN ? p.n - n0 : S::BN;
@@ -184,33 +191,13 @@ __global__ __launch_bounds__(S::THREADS) void i8_gemm_kernel(I8GemmArgs g) {
   for (int i = 0; i < S::TM; ++i)
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) acc[i][j] = i32x16{};
+  I8Scales<S> scales;
+  scales.load([&](int i) { return m0 + (i < rows ? i : rows - 1); }, [&](int, int row) { return p.sx[row]; },
+              [&](int i) { return p.sw[n0 + (i < cols ? i : cols - 1)]; },
+              [&](int i) { return p.bias ? p.bias[n0 + (i < cols ? i : cols - 1)] : 0.0f; });
   i8_tile<S, false>(p.x + (size_t)m0 * p.k, [&](int i) { return i < rows ? i : rows - 1; }, p.w + (size_t)n0 * p.k,
-             p.w, [&](int i) { return i < cols ? i : cols - 1; }, p.k, 0, (p.k + kI8Step - 1) / kI8Step, lds, acc);
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  const bool wide = p.n % 4 == 0 && ((uintptr_t)p.y & (p.y_type == kI8F32 ? 15 : 7)) == 0;
-#pragma unroll
-  for (int i = 0; i < S::TM; ++i) {
-    const int r = (wm * S::TM + i) * 32 + (lane & 31);
-    if (r >= rows) continue;
-    const float sx = p.sx[m0 + r];
-    const size_t row = (size_t)(m0 + r) * p.n + n0;
-#pragma unroll
-    for (int j = 0; j < S::TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = (wn * S::TN + j) * 32 + 8 * q + 4 * (lane >> 5);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int cc = n0 + (c + e < cols ? c + e : cols - 1);
-          v[e] = (float)acc[i][j][4 * q + e] * sx * p.sw[cc];
-          if (p.bias) v[e] += p.bias[cc];
-        }
-        i8_store(p.y, row + c, p.y_type, v, cols - c, wide);
-      }
-  }
+                    p.w, [&](int i) { return i < cols ? i : cols - 1; }, p.k, 0, (p.k + S::BK - 1) / S::BK, lds, acc);
+  i8_finish<S, false>(acc, scales, lds, p.y, p.y_type, p.bias != nullptr, p.n, n0, rows, cols);
 }
 
 template <class S>
@@ -225,8 +212,67 @@ static hipError_t launch_shape(I8GemmArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Tile shapes and what a tile costs alone on its CU (shapes of 160 KB / LDS > 1:
+// with that many beside it): `fixed` us and `step` us for 128 bytes of k.  Measured on
+// products with cold weights (m x n x k, us with about 4 us of launch):
+//   shape        512x2560x4096  512x9728x2560  1024x9728x2560  2048x2560x9728  2048x9728x2560  16384x2560x9728
+//   64 x 64               22.9           35.1            58.8            97.1             103              692
+//   64 x 128              19.9           41.1            64.5           101.8             123                -
+//   128 x 128             24.4           38.4            54.9            94.2              87              456
+//   128 x 192             29.0           25.7            47.0            62.6              81                -
+//   256 x 192             45.7           38.8            39.6           102.9              74              432
+//   256 x 256             54.8           44.7            45.1           123.0              80              403
+//   256 x 320             62.6           49.2            49.7           137.1              57              349
+// A larger tile moves fewer bytes for its products; which one is best is mostly a
+// matter of how evenly its tiles fall on the 256 CUs.
+struct I8Choice {
+  int bm, bn, at_once;  // tiles a CU holds
+  float fixed, step;
+};
+constexpr I8Choice kI8Choices[] = {
+    {64, 64, 3, 3.0f, 0.55f},  {64, 128, 1, 3.0f, 0.45f},  {128, 128, 1, 4.0f, 0.60f}, {128, 192, 1, 5.0f, 0.75f},
+    {256, 192, 1, 7.0f, 1.25f}, {256, 256, 1, 8.0f, 1.52f}, {256, 320, 1, 9.0f, 1.72f},
+};
+constexpr int kI8Shapes = sizeof(kI8Choices) / sizeof(kI8Choices[0]);
+
+static int i8_choose(const I8GemmArgs& g) {
+  if (const char* env = getenv("QMM_I8_FORCE")) {  // tuning sweeps and tests: a shape by its place
+    const int f = atoi(env);
+    if (f >= 0 && f < kI8Shapes) return f;
+  }
+  int best = 0;
+  double least = 1e30;
+  for (int c = 0; c < kI8Shapes; ++c) {
+    const I8Choice& h = kI8Choices[c];
+    double tiles = 0, steps = 0;
+    for (int i = 0; i < g.count; ++i) {
+      const double t = (double)((g.p[i].m + h.bm - 1) / h.bm) * ((g.p[i].n + h.bn - 1) / h.bn);
+      tiles += t;
+      steps += t * ((g.p[i].k + 127) / 128);
+    }
+    const double slots = 256.0 * h.at_once;
+    const double rounds = (double)(long)((tiles + slots - 1) / slots);
+    // fewer tiles than places: they share a CU with fewer others
+    const double share = tiles < slots && h.at_once > 1 ? 0.5 + 0.5 * tiles / slots : 1.0;
+    const double cost = rounds * (h.fixed + h.step * share * steps / tiles);
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
+  return best;
+}
+
 hipError_t launch_i8_gemm(I8GemmArgs& g, hipStream_t st) {
-  return launch_shape<I8Shape<64, 64, 2, 2, 2>>(g, st);
+  switch (i8_choose(g)) {
+    case 0: return launch_shape<I8Shape<64, 64, 2, 2, 3, 128>>(g, st);
+    case 1: return launch_shape<I8Shape<64, 128, 2, 4, 6, 128>>(g, st);
+    case 2: return launch_shape<I8Shape<128, 128, 2, 4, 3, 128>>(g, st);
+    case 3: return launch_shape<I8Shape<128, 192, 4, 2, 3, 128>>(g, st);
+    case 4: return launch_shape<I8Shape<256, 192, 4, 2, 2, 128>>(g, st);
+    case 5: return launch_shape<I8Shape<256, 256, 2, 4, 2, 128>>(g, st);
+    default: return launch_shape<I8Shape<256, 320, 4, 2, 2, 128>>(g, st);
+  }
 }
 
 }  // namespace qmm

@@ -2,6 +2,8 @@
 // qmm_i8_moe_gate_up_swiglu) from a routing plan of qmm_moe_route: each
 // workgroup takes rows of one expert from the plan's list, gathers their codes
 // and multiplies them by that expert's weights.
+#include <stdlib.h>
+
 #include "i8_core.h"
 #include "moe_plan.h"
 #include "qmm_internal.h"
@@ -20,15 +22,10 @@ __device__ __forceinline__ void i8_nan_rows(const I8MoeArgs& g, const int32_t* s
   else fill_nan_rows(static_cast<uint16_t*>(g.y), sorted, mt, c0, bn, g.n, (uint16_t)(g.y_type == kI8F16 ? 0x7E00 : 0x7FC0));
 }
 
-// GATED: the tile's rows of W are half gate, half up: a wave's first TN / 2
-// blocks of columns are gate's and the others the same columns of up, so both
-// products of an output stand in the same lane and register.
 template <class S, bool GATED>
 __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_tiles) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
-  __shared__ int32_t pair_of[S::BM];
   constexpr int BC = GATED ? S::BN / 2 : S::BN;  // output columns
-  constexpr int TC = GATED ? S::TN / 2 : S::TN;
   const int32_t* ws = g.plan;
   const int pairs = g.t * g.top_k;
   int tile, tn;
@@ -40,20 +37,42 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
     i8_nan_all(g);
     return;
   }
-  if (tile >= ws[0]) return;
-  MoeTile mt = reinterpret_cast<const MoeTile*>(ws + kPlanHeaderInts + pairs)[tile];
-  mt.start += sub * S::BM;
-  mt.rows -= sub * S::BM;
-  if (mt.rows <= 0) return;
-  if (mt.rows > S::BM) mt.rows = S::BM;
+  const int listed = __builtin_amdgcn_readfirstlane(ws[0]);
+  if (tile >= listed) return;
+  const MoeTile* list = reinterpret_cast<const MoeTile*>(ws + kPlanHeaderInts + pairs);
+  MoeTile mt = list[tile];  // one tile of the workgroup: in scalar registers
+  mt.expert = __builtin_amdgcn_readfirstlane(mt.expert);
+  mt.start = __builtin_amdgcn_readfirstlane(mt.start);
+  mt.rows = __builtin_amdgcn_readfirstlane(mt.rows);
+  if (g.plan_rows < S::BM) {
+    // several of the list's tiles at once, from every `span`-th of an expert's;
+    // the expert's tiles stand together, all but the last whole
+    const int span = S::BM / g.plan_rows;
+    const int lane = threadIdx.x & 63;
+    int before = 0;  // tiles of the same expert before this one
+    for (int first = tile - 1;; first -= 64) {  // ends at the list's first
+      const int i = first - lane;
+      const uint64_t other = __ballot(i < 0 || list[i < 0 ? 0 : i].expert != mt.expert);
+      before += other ? __builtin_ctzll(other) : 64;
+      if (other) break;
+    }
+    if (before % span) return;
+    for (int i = 1; i < span && tile + i < listed; ++i)
+      if (list[tile + i].expert == mt.expert) mt.rows += list[tile + i].rows;
+    mt.rows = __builtin_amdgcn_readfirstlane(mt.rows);
+  } else {
+    mt.start += sub * S::BM;
+    mt.rows -= sub * S::BM;
+    if (mt.rows <= 0) return;
+    if (mt.rows > S::BM) mt.rows = S::BM;
+  }
   const int32_t* sorted = ws + kPlanHeaderInts;
   const int n0 = tn * BC;
   if (mt.expert < 0) {
     i8_nan_rows(g, sorted, mt, n0, BC);
     return;
   }
-  for (int i = threadIdx.x; i < S::BM; i += S::THREADS) pair_of[i] = sorted[mt.start + (i < mt.rows ? i : mt.rows - 1)];
-  __syncthreads();
+  sorted += mt.start;
   const int cols = g.n - n0 < BC ? g.n - n0 : BC;
   const size_t at = ((size_t)mt.expert * g.n + n0) * g.k;
   i32x16 acc[S::TM][S::TN];
@@ -61,37 +80,20 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
   for (int i = 0; i < S::TM; ++i)
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) acc[i][j] = i32x16{};
-  auto x_row = [&](int i) { const int p = pair_of[i]; return g.a_row_per_pair ? p : p / g.top_k; };
-  i8_tile<S, GATED>(g.x, x_row, g.w + at, GATED ? g.w2 + at : g.w + at,
-                    [&](int i) { return i < cols ? i : cols - 1; }, g.k, 0, (g.k + kI8Step - 1) / kI8Step, lds, acc);
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  const bool wide = g.n % 4 == 0 && ((uintptr_t)g.y & (g.y_type == kI8F32 ? 15 : 7)) == 0;
-  const float* sw = g.sw + (size_t)mt.expert * g.n + n0;
-  const float* sw2 = GATED ? g.sw2 + (size_t)mt.expert * g.n + n0 : nullptr;
-#pragma unroll
-  for (int i = 0; i < S::TM; ++i) {
-    const int r = (wm * S::TM + i) * 32 + (lane & 31);
-    if (r >= mt.rows) continue;
-    const int pair = pair_of[r];
-    const float sx = g.sx[g.a_row_per_pair ? pair : pair / g.top_k];
-    const size_t row = (size_t)pair * g.n + n0;
-#pragma unroll
-    for (int j = 0; j < TC; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = (wn * TC + j) * 32 + 8 * q + 4 * (lane >> 5);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int cc = c + e < cols ? c + e : cols - 1;
-          v[e] = (float)acc[i][j][4 * q + e] * sx * sw[cc];
-          if constexpr (GATED) v[e] = i8_silu(v[e]) * ((float)acc[i][j + TC][4 * q + e] * sx * sw2[cc]);
-        }
-        i8_store(g.y, row + c, g.y_type, v, cols - c, wide);
-      }
-  }
+  auto pair = [&](int i) { return sorted[i < mt.rows ? i : mt.rows - 1]; };
+  auto row = [&](int p) { return g.a_row_per_pair ? p : p / g.top_k; };
+  I8Scales<S> scales;
+  const size_t column = (size_t)mt.expert * g.n + n0;
+  scales.load(pair, [&](int, int p) { return g.sx[row(p)]; },
+              [&](int i) {
+                const bool up = GATED && i % 32 >= 16;
+                if (GATED) i = i / 32 * 16 + i % 16;
+                return (up ? g.sw2 : g.sw)[column + (i < cols ? i : cols - 1)];
+              },
+              [](int) { return 0.0f; });
+  i8_tile<S, GATED>(g.x, [&](int i) { return row(pair(i)); }, g.w + at, GATED ? g.w2 + at : g.w + at,
+                    [&](int i) { return i < cols ? i : cols - 1; }, g.k, 0, (g.k + S::BK - 1) / S::BK, lds, acc);
+  i8_finish<S, GATED>(acc, scales, lds, g.y, g.y_type, false, g.n, n0, mt.rows, cols);
 }
 
 template <class S, bool GATED>
@@ -104,10 +106,24 @@ static hipError_t launch_moe_shape(I8MoeArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Tile shapes, us a call (plan rows 32: 64 tokens, way back; 64: 2048 tokens, way
+// back; 128: 16384 tokens, gate and up; 128 experts, top-8, 768 x 2048, rounding of
+// the rows included):
+//   plan   64x128   64x256   128x128   128x192   256x192   256x256
+//     32     29.1     26.0      29.8      31.9      42.6      37.8
+//     64    103.0     98.3     104.7      98.2     126.8     115.2
+//    128    625.6    576.6     547.7     499.5     574.9     609.1
+// Two workgroups a CU (80 KB of LDS each) beat larger tiles: one stores while the
+// other multiplies.
 hipError_t launch_i8_moe(I8MoeArgs& g, hipStream_t st) {
-  using S = I8Shape<32, 128, 1, 4, 2>;
-  using D = I8Shape<32, 256, 1, 4, 2>;
-  return g.w2 ? launch_moe_shape<D, true>(g, st) : launch_moe_shape<S, false>(g, st);
+  bool tall = g.plan_rows >= 128;
+  if (const char* env = getenv("QMM_I8_MOE_FORCE")) tall = atoi(env) != 0;  // tuning sweeps and tests
+  if (tall) {
+    using S = I8Shape<128, 192, 4, 2, 2, 128>;
+    return g.w2 ? launch_moe_shape<S, true>(g, st) : launch_moe_shape<S, false>(g, st);
+  }
+  using S = I8Shape<64, 256, 2, 4, 2, 128>;
+  return g.w2 ? launch_moe_shape<S, true>(g, st) : launch_moe_shape<S, false>(g, st);
 }
 
 }  // namespace qmm

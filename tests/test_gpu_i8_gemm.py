@@ -114,8 +114,46 @@ SIZES = [(1, 1, 16), (1, 7, 48), (1, 1000, 2560), (2, 33, 64), (3, 64, 112), (4,
          (1030, 129, 176), (1, 40, 131008), (70, 4, 32)]
 
 
+SHAPES = 7  # tile shapes a product can take
+
+
 @pytest.mark.parametrize("m,n,k", SIZES)
 def test_products_of_codes(m, n, k):
+    codes_case(m, n, k)
+
+
+@pytest.mark.parametrize("shape", range(SHAPES))
+@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (65, 330, 112), (129, 387, 528), (257, 260, 1296), (513, 770, 352),
+                                   (700, 1300, 272), (300, 2049, 128)])
+def test_products_by_every_tile_shape(m, n, k, shape, monkeypatch):
+    monkeypatch.setenv("QMM_I8_FORCE", str(shape))
+    codes_case(m, n, k)
+
+
+@pytest.mark.parametrize("shape", range(SHAPES))
+@pytest.mark.parametrize("yt", FLOATS, ids=ids)
+def test_outputs_of_every_type_by_every_tile_shape(yt, shape, monkeypatch):
+    """Widths that take whole pieces in every type, in some and in none, and a y
+    off 16 bytes."""
+    monkeypatch.setenv("QMM_I8_FORCE", str(shape))
+    say("i8 gemm outputs", yt, shape)
+    r = np.random.default_rng([21, shape])
+    for n in (328, 332, 333):
+        w, ws = weights(r, n, 80)
+        b = r.standard_normal(n).astype(np.float32)
+        x = activations(r, 270, 80, BF16)
+        want = ref.product_f64(*ref.rows_f64(f64(x)), w, ws, b)
+        y = Guarded((270, n), yt)
+        qmm.i8_gemm(dev(w), dev(ws), x, bias=dev(b), y=y.t)
+        off = torch.zeros(270 * n + 1, dtype=yt, device="cuda")
+        qmm.i8_gemm(dev(w), dev(ws), x, bias=dev(b), y=off[1:].view(270, n))
+        torch.cuda.synchronize()
+        y.check(n)
+        ref.check(f64(y.t), want, yt, n)
+        assert torch.equal(off[1:].view(270, n), y.t) and off[0] == 0
+
+
+def codes_case(m, n, k):
     say("i8 gemm codes", m, n, k)
     r = np.random.default_rng([5, m, n, k])
     w, ws = weights(r, n, k)

@@ -52,7 +52,7 @@ SIZES = [(1, 1, 1, 1, 16, "any"), (1, 8, 128, 768, 256, "any"), (3, 2, 5, 33, 48
          (17, 8, 8, 65, 1040, "any"), (40, 3, 60, 100, 272, "few"), (33, 2, 4, 257, 208, "one"),
          (64, 8, 16, 128, 384, "bad"), (100, 8, 10, 515, 80, "any"), (160, 8, 8, 64, 640, "any"),
          (300, 4, 6, 96, 1296, "any"), (333, 4, 60, 517, 112, "few"), (512, 8, 9, 31, 128, "bad"), (2, 8, 4, 40, 64, "any"),
-         (1000, 1, 3, 129, 96, "any")]
+         (1000, 1, 3, 129, 96, "any"), (2000, 2, 7, 200, 144, "any"), (3000, 1, 5, 97, 48, "bad")]
 
 
 @pytest.mark.parametrize("t,top_k,e,n,k,kind", SIZES)
@@ -91,6 +91,24 @@ def test_gate_and_up(t, top_k, e, n, k, kind, xt, ht):
     torch.cuda.synchronize()
     h.check("h")
     ref.check(f64(h.t), want([gate, up], ref.rows_f64(f64(x)), I, False), ht, (t, top_k, e, n, k))
+
+
+@pytest.mark.parametrize("shape", [0, 1])
+@pytest.mark.parametrize("t,top_k,e,n,k,kind", SIZES)
+def test_both_tile_shapes(t, top_k, e, n, k, kind, shape, monkeypatch):
+    """A tile may take part of a row tile of the plan, one, or several."""
+    monkeypatch.setenv("QMM_I8_MOE_FORCE", str(shape))
+    test_grouped_products(t, top_k, e, n, k, kind, True)
+    test_gate_and_up(t, top_k, e, n, k, kind, F16, BF16)
+
+
+@pytest.mark.parametrize("rows", [32, 64, 128, 160])
+@pytest.mark.parametrize("shape", [0, 1])
+def test_plans_of_every_row_tile(rows, shape, monkeypatch):
+    monkeypatch.setenv("QMM_MOE_FORCE", f"{rows},1")
+    monkeypatch.setenv("QMM_I8_MOE_FORCE", str(shape))
+    for size in [(100, 8, 10, 70, 80, "few"), (900, 2, 6, 30, 48, "bad"), (2, 2, 3, 20, 64, "any")]:
+        test_grouped_products(*size, False)
 
 
 @pytest.mark.parametrize("yt", [F32, F16, BF16], ids=ids)
