@@ -3,92 +3,16 @@
 #include <stdlib.h>
 
 #include "i8_core.h"
+#include "i8_few.h"
+#include "i8_round.h"
 #include "qmm_internal.h"
 
 namespace qmm {
 
 // ---------------------------------------------------------------- rounding
-// s = fp32(max |x| / 127), q = rint(x / s): which whole number is nearest to
-// the exact quotient, ties to even.  n = rint(x * (1 / s)) is that number or its
-// neighbour; the remainder x - n s is a multiple of half a unit in the last
-// place of s and not much larger than s / 2, so one fma gives it exactly and it
-// decides.  A row whose largest magnitude is below 2^-119 (where s would
-// leave fp32's normal range) has s = 0 and codes 0; one with a NaN or infinity
-// has s = NaN and codes 0.
-//
 // Sixteen values a lane: one 16-byte store of codes, two (16-bit x) or four
 // (fp32 x) 16-byte loads.  A row is taken by WPR waves, which hold it in registers
 // up to 16 * 64 * WPR * R values; what is longer is read a second time.
-
-__device__ __forceinline__ void i8_load16(const void* x, size_t at, int type, float (&v)[16]) {
-  if (type == kI8F32) {
-    auto p = to_global(reinterpret_cast<const u32x4*>(static_cast<const float*>(x) + at));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 u = p[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(u[j]);
-    }
-    return;
-  }
-  auto p = to_global(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at));
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const u32x4 u = p[i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * i + 2 * j] = type == kI8F16 ? f16_bits_to_f32((uint16_t)u[j]) : __uint_as_float(u[j] << 16);
-      v[8 * i + 2 * j + 1] = type == kI8F16 ? f16_bits_to_f32((uint16_t)(u[j] >> 16)) : __uint_as_float(u[j] & 0xFFFF0000u);
-    }
-  }
-}
-
-__device__ __forceinline__ int i8_round(float x, float s, float inv) {
-  const float n = rintf(x * inv);
-  const float d = fmaf(-n, s, x);
-  const float h = 0.5f * s;
-  const int i = (int)n;
-  const int up = d > h || (d == h && (i & 1));
-  const int down = d < -h || (d == -h && (i & 1));
-  return i + up - down;
-}
-
-__device__ __forceinline__ i32x4 i8_round16(const float (&v)[16], float s, float inv) {
-  i32x4 q;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w |= (uint32_t)(i8_round(v[4 * i + j], s, inv) & 0xFF) << (8 * j);
-    q[i] = (int)w;
-  }
-  return q;
-}
-
-__device__ __forceinline__ uint32_t i8_top(const float (&v)[16], uint32_t top) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t u = __float_as_uint(v[i]) & 0x7FFFFFFFu;  // ordered like the magnitude, NaN above infinity
-    top = u > top ? u : top;
-  }
-  return top;
-}
-
-// Scale of a row from the bits of its largest magnitude; 0 and NaN have codes 0.
-__device__ __forceinline__ float i8_scale(uint32_t top) {
-  if (top >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  if (top < 0x04000000u) return 0.0f;  // 2^-119
-  return __fdiv_rn(__uint_as_float(top), 127.0f);
-}
-
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const uint32_t u = __shfl_xor((int)v, d, 64);
-    v = u > v ? u : v;
-  }
-  return v;
-}
 
 constexpr int kI8RoundThreads = 256;
 
@@ -195,7 +119,7 @@ __global__ __launch_bounds__(S::THREADS) void i8_gemm_kernel(I8GemmArgs g) {
   scales.load([&](int i) { return m0 + (i < rows ? i : rows - 1); }, [&](int, int row) { return p.sx[row]; },
               [&](int i) { return p.sw[n0 + (i < cols ? i : cols - 1)]; },
               [&](int i) { return p.bias ? p.bias[n0 + (i < cols ? i : cols - 1)] : 0.0f; });
-  i8_tile<S, false>(p.x + (size_t)m0 * p.k, [&](int i) { return i < rows ? i : rows - 1; }, p.w + (size_t)n0 * p.k,
+  i8_tile<S, false>(static_cast<const int8_t*>(p.x) + (size_t)m0 * p.k, [&](int i) { return i < rows ? i : rows - 1; }, p.w + (size_t)n0 * p.k,
                     p.w, [&](int i) { return i < cols ? i : cols - 1; }, p.k, 0, (p.k + S::BK - 1) / S::BK, lds, acc);
   i8_finish<S, false>(acc, scales, lds, p.y, p.y_type, p.bias != nullptr, p.n, n0, rows, cols);
 }
@@ -236,10 +160,6 @@ constexpr I8Choice kI8Choices[] = {
 constexpr int kI8Shapes = sizeof(kI8Choices) / sizeof(kI8Choices[0]);
 
 static int i8_choose(const I8GemmArgs& g) {
-  if (const char* env = getenv("QMM_I8_FORCE")) {  // tuning sweeps and tests: a shape by its place
-    const int f = atoi(env);
-    if (f >= 0 && f < kI8Shapes) return f;
-  }
   int best = 0;
   double least = 1e30;
   for (int c = 0; c < kI8Shapes; ++c) {
@@ -263,8 +183,89 @@ static int i8_choose(const I8GemmArgs& g) {
   return best;
 }
 
-hipError_t launch_i8_gemm(I8GemmArgs& g, hipStream_t st) {
-  switch (i8_choose(g)) {
+template <int U, bool LOOP, int TYPE>
+__global__ __launch_bounds__(kI8FewThreads) __attribute__((amdgpu_waves_per_eu(4))) void i8_few_kernel(I8GemmArgs g, int kw) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  int b = blockIdx.x, which = 0;
+  while (which + 1 < g.count && b >= g.p[which + 1].first) ++which;
+  const I8Problem& p = g.p[which];
+  const int wide = 16 * (kI8FewWaves / kw), n0 = (b - p.first) * wide;
+  const I8FewTile t{p.w + (size_t)n0 * p.k, nullptr, p.sw + n0, nullptr, p.bias ? p.bias + n0 : nullptr, p.x, p.sx, p.y,
+                    p.y_type, p.n, n0, p.n - n0 < wide ? p.n - n0 : wide, p.m, p.k, kw};
+  auto same = [](int i) { return i; };
+  i8_few<U, LOOP, false, TYPE>(t, lds, same, same);
+}
+
+template <int U, bool LOOP, int TYPE>
+static hipError_t launch_few_kernel(I8GemmArgs& g, int kw, hipStream_t st) {
+  long blocks = 0;
+  size_t lds = 0;
+  const int wide = 16 * (kI8FewWaves / kw);
+  for (int i = 0; i < g.count; ++i) {
+    g.p[i].first = (int)blocks;
+    blocks += (g.p[i].n + wide - 1) / wide;
+    const size_t need = i8_few_lds<U, false>(TYPE == kI8Codes ? 0 : g.p[i].m, g.p[i].k);
+    lds = need > lds ? need : lds;
+  }
+  hipLaunchKernelGGL((i8_few_kernel<U, LOOP, TYPE>), dim3((unsigned)blocks), dim3(kI8FewThreads), lds, st, g, kw);
+  return hipGetLastError();
+}
+
+static long i8_blocks(const I8GemmArgs& g) {  // of 16 columns
+  long blocks = 0;
+  for (int i = 0; i < g.count; ++i) blocks += (g.p[i].n + 15) / 16;
+  return blocks;
+}
+
+template <int TYPE>
+static hipError_t launch_few(I8GemmArgs& g, hipStream_t st) {
+  int most = 0;
+  for (int i = 0; i < g.count; ++i) most = g.p[i].k > most ? g.p[i].k : most;
+  const int kw = i8_few_kw(i8_blocks(g), TYPE == kI8Codes);
+  const int each = ((most + 63) / 64 + kw - 1) / kw;  // slices a wave
+  if (each <= 2) return launch_few_kernel<2, false, TYPE>(g, kw, st);
+  if (each <= 5) return launch_few_kernel<5, false, TYPE>(g, kw, st);
+  if constexpr (TYPE != kI8Codes)
+    if (each <= 8) return launch_few_kernel<8, false, TYPE>(g, kw, st);
+  return launch_few_kernel<5, true, TYPE>(g, kw, st);
+}
+
+// How a call runs, decided once: `staged` (the product rounds x itself) goes with
+// few rows only.  us of a call, rounding of fp16 x included (graph, cold weights):
+//   rows x n x k          rounded in the product   few rows, codes   tiles of 64 x 64
+//    1 x 9728 x 2560                 9.6                 14.2              17.0
+//    4 x 9728 x 2560                12.2                 14.6              17.3
+//    4 x 2560 x 9728                   -                 17.2              36.8
+//    8 x 1024 x 1024                 4.4                  6.7               8.4
+//    8 x 151936 x 1024              34.6                 41.4              38.2
+//   16 x 9728 x 2560                   -                 16.4              17.5
+//   16 x 151936 x 1024                 -                 46.9              39.4
+I8Way i8_gemm_way(const I8GemmArgs& g) {
+  I8Way way{false, false, 0};
+  const char* force = getenv("QMM_I8_FORCE");  // tuning sweeps and tests: a tile shape by its place
+  if (force != nullptr && atoi(force) >= 0 && atoi(force) < kI8Shapes) {
+    way.shape = atoi(force);
+    return way;
+  }
+  int most = 0;
+  way.staged = true;
+  for (int i = 0; i < g.count; ++i) {
+    most = g.p[i].m > most ? g.p[i].m : most;
+    if (g.p[i].x_type == kI8Codes || g.p[i].x_type != g.p[0].x_type || !i8_can_stage(g.p[i].m, g.p[i].k)) way.staged = false;
+  }
+  way.few = way.staged || (most <= kI8FewRows && i8_blocks(g) <= 1024);
+  if (!way.few) way.shape = i8_choose(g);
+  return way;
+}
+
+hipError_t launch_i8_gemm(I8GemmArgs& g, I8Way way, hipStream_t st) {
+  if (way.few) switch (g.p[0].x_type) {
+    case kI8F32: return launch_few<kI8F32>(g, st);
+    case kI8F16: return launch_few<kI8F16>(g, st);
+    case kI8BF16: return launch_few<kI8BF16>(g, st);
+    default: return launch_few<kI8Codes>(g, st);
+  }
+  switch (way.shape) {
     case 0: return launch_shape<I8Shape<64, 64, 2, 2, 3, 128>>(g, st);
     case 1: return launch_shape<I8Shape<64, 128, 2, 4, 6, 128>>(g, st);
     case 2: return launch_shape<I8Shape<128, 128, 2, 4, 3, 128>>(g, st);

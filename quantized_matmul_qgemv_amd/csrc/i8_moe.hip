@@ -4,7 +4,7 @@
 // and multiplies them by that expert's weights.
 #include <stdlib.h>
 
-#include "i8_core.h"
+#include "i8_few.h"
 #include "moe_plan.h"
 #include "qmm_internal.h"
 
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
                 return (up ? g.sw2 : g.sw)[column + (i < cols ? i : cols - 1)];
               },
               [](int) { return 0.0f; });
-  i8_tile<S, GATED>(g.x, [&](int i) { return row(pair(i)); }, g.w + at, GATED ? g.w2 + at : g.w + at,
+  i8_tile<S, GATED>(static_cast<const int8_t*>(g.x), [&](int i) { return row(pair(i)); }, g.w + at, GATED ? g.w2 + at : g.w + at,
                     [&](int i) { return i < cols ? i : cols - 1; }, g.k, 0, (g.k + S::BK - 1) / S::BK, lds, acc);
   i8_finish<S, GATED>(acc, scales, lds, g.y, g.y_type, false, g.n, n0, mt.rows, cols);
 }
@@ -106,6 +106,81 @@ static hipError_t launch_moe_shape(I8MoeArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Few rows an expert: 16 * 8 / kw columns of one row tile a workgroup.
+template <int U, bool LOOP, bool GATED, int TYPE>
+__global__ __launch_bounds__(kI8FewThreads) __attribute__((amdgpu_waves_per_eu(4))) void i8_moe_few_kernel(I8MoeArgs g, int n_tiles, int kw) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int32_t* ws = g.plan;
+  const int pairs = g.t * g.top_k;
+  if (ws[1] != g.plan_rows || ws[2] != pairs || ws[3] != g.e) {
+    i8_nan_all(g);
+    return;
+  }
+  const int tile = blockIdx.x / n_tiles, tn = blockIdx.x % n_tiles;
+  if (tile >= ws[0]) return;
+  MoeTile mt = reinterpret_cast<const MoeTile*>(ws + kPlanHeaderInts + pairs)[tile];
+  mt.expert = __builtin_amdgcn_readfirstlane(mt.expert);
+  mt.start = __builtin_amdgcn_readfirstlane(mt.start);
+  mt.rows = __builtin_amdgcn_readfirstlane(mt.rows);
+  const int32_t* sorted = ws + kPlanHeaderInts;
+  const int wide = 16 * (kI8FewWaves / kw), n0 = tn * wide;
+  if (mt.expert < 0) {
+    i8_nan_rows(g, sorted, mt, n0, wide);
+    return;
+  }
+  sorted += mt.start;
+  const size_t column = (size_t)mt.expert * g.n + n0, at = column * g.k;
+  const I8FewTile t{g.w + at, GATED ? g.w2 + at : nullptr, g.sw + column, GATED ? g.sw2 + column : nullptr, nullptr, g.x, g.sx, g.y,
+                    g.y_type, g.n, n0, g.n - n0 < wide ? g.n - n0 : wide, mt.rows, g.k, kw};
+  auto pair = [&](int i) { return sorted[i]; };
+  auto row = [&](int i) { const int p = sorted[i]; return g.a_row_per_pair ? p : p / g.top_k; };
+  i8_few<U, LOOP, GATED, TYPE>(t, lds, row, pair);
+}
+
+template <int U, bool LOOP, bool GATED, int TYPE>
+static hipError_t launch_moe_few_kernel(I8MoeArgs& g, int kw, hipStream_t st) {
+  const int wide = 16 * (kI8FewWaves / kw), n_tiles = (g.n + wide - 1) / wide;
+  const int pairs = g.t * g.top_k, tiles = max_row_tiles(pairs, g.e, g.plan_rows);
+  const size_t lds = i8_few_lds<U, GATED>(TYPE == kI8Codes ? 0 : pairs, g.k);
+  hipLaunchKernelGGL((i8_moe_few_kernel<U, LOOP, GATED, TYPE>), dim3((unsigned)tiles * n_tiles), dim3(kI8FewThreads), lds, st, g,
+                     n_tiles, kw);
+  return hipGetLastError();
+}
+
+template <bool GATED, int TYPE>
+static hipError_t launch_moe_few(I8MoeArgs& g, hipStream_t st) {
+  const long pairs = (long)g.t * g.top_k, tiles = pairs < g.e ? pairs : g.e;  // about as many as have rows
+  const int kw = i8_few_kw(tiles * ((g.n + 15) / 16), TYPE == kI8Codes);
+  const int each = ((g.k + 63) / 64 + kw - 1) / kw;
+  if (each <= 2) return launch_moe_few_kernel<2, false, GATED, TYPE>(g, kw, st);
+  if (each <= 4) return launch_moe_few_kernel<4, false, GATED, TYPE>(g, kw, st);
+  return launch_moe_few_kernel<4, true, GATED, TYPE>(g, kw, st);
+}
+
+template <bool GATED>
+static hipError_t launch_moe_few_type(I8MoeArgs& g, hipStream_t st) {
+  switch (g.x_type) {
+    case kI8F32: return launch_moe_few<GATED, kI8F32>(g, st);
+    case kI8F16: return launch_moe_few<GATED, kI8F16>(g, st);
+    case kI8BF16: return launch_moe_few<GATED, kI8BF16>(g, st);
+    default: return launch_moe_few<GATED, kI8Codes>(g, st);
+  }
+}
+
+// How a call runs, decided once: few rows, where no row tile can have more than 16
+// (`staged`: not more than a workgroup rounds for itself), or tiles.  One token, 8 of
+// 128 experts, gate and up of 768 x 2048: 9.7 us, as codes 13.4, in tiles 29.6.
+I8Way i8_moe_way(const I8MoeArgs& g) {
+  const long pairs = (long)g.t * g.top_k;
+  I8Way way{pairs <= kI8FewRows, false, g.plan_rows >= 128 ? 1 : 0};
+  if (const char* env = getenv("QMM_I8_MOE_FORCE")) {  // tuning sweeps and tests
+    way.few = false;
+    way.shape = atoi(env) != 0;
+  }
+  way.staged = way.few && g.x_type != kI8Codes && i8_can_stage((int)pairs, g.k);
+  return way;
+}
+
 // Tile shapes, us a call (plan rows 32: 64 tokens, way back; 64: 2048 tokens, way
 // back; 128: 16384 tokens, gate and up; 128 experts, top-8, 768 x 2048, rounding of
 // the rows included):
@@ -115,10 +190,9 @@ static hipError_t launch_moe_shape(I8MoeArgs& g, hipStream_t st) {
 //    128    625.6    576.6     547.7     499.5     574.9     609.1
 // Two workgroups a CU (80 KB of LDS each) beat larger tiles: one stores while the
 // other multiplies.
-hipError_t launch_i8_moe(I8MoeArgs& g, hipStream_t st) {
-  bool tall = g.plan_rows >= 128;
-  if (const char* env = getenv("QMM_I8_MOE_FORCE")) tall = atoi(env) != 0;  // tuning sweeps and tests
-  if (tall) {
+hipError_t launch_i8_moe(I8MoeArgs& g, I8Way way, hipStream_t st) {
+  if (way.few) return g.w2 ? launch_moe_few_type<true>(g, st) : launch_moe_few_type<false>(g, st);
+  if (way.shape == 1) {
     using S = I8Shape<128, 192, 4, 2, 2, 128>;
     return g.w2 ? launch_moe_shape<S, true>(g, st) : launch_moe_shape<S, false>(g, st);
   }

@@ -851,30 +851,38 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
       return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
     CHECK_PTR(workspace, 16);
   }
-  qmm::I8QuantizeArgs qa{};
   qmm::I8GemmArgs g{};
-  char* next = static_cast<char*>(workspace);
-  int at[qmm::kI8MaxProblems];  // of a problem's codes: its place in qa
+  int from[qmm::kI8MaxProblems];  // the problem that a place of g came from
   for (int i = 0; i < count; ++i) {
     const qmm_i8_problem& q = problems[i];
     if (q.m == 0) continue;
-    qmm::I8Problem& p = g.p[g.count++];
-    p = qmm::I8Problem{static_cast<const int8_t*>(q.x), q.x_scales, q.w, q.w_scales, q.bias, q.y, q.m, q.n, q.k, q.y_type, 0};
-    if (q.x_type == QMM_I8) continue;
-    const int from = i8_first_of(problems, i);
-    if (from == i) {
-      at[i] = qa.count;
-      qa.job[qa.count++] = qmm::I8QuantizeJob{q.x, reinterpret_cast<int8_t*>(next),
-                                              reinterpret_cast<float*>(next + up256((size_t)q.m * q.k)), q.m, q.k, q.x_type, 0};
-      next += i8_codes_bytes(q.m, q.k);
-    }
-    p.x = qa.job[at[from]].codes;
-    p.sx = qa.job[at[from]].scales;
+    from[g.count] = i;
+    g.p[g.count++] = qmm::I8Problem{q.x, q.x_scales, q.w, q.w_scales, q.bias, q.y, q.m, q.n, q.k, q.x_type, q.y_type, 0};
   }
   if (g.count == 0) return QMM_OK;
-  if (qa.count > 0)
-    if (int st = hip_status(qmm::launch_i8_quantize(qa, (hipStream_t)stream), fn)) return st;
-  return hip_status(qmm::launch_i8_gemm(g, (hipStream_t)stream), fn);
+  const qmm::I8Way way = qmm::i8_gemm_way(g);
+  if (!way.staged) {
+    qmm::I8QuantizeArgs qa{};
+    char* next = static_cast<char*>(workspace);
+    int job[qmm::kI8MaxProblems];  // of a problem's x
+    for (int i = 0; i < g.count; ++i) {
+      qmm::I8Problem& p = g.p[i];
+      if (p.x_type == QMM_I8) continue;
+      const int same = i8_first_of(problems, from[i]);
+      if (same == from[i]) {
+        job[same] = qa.count;
+        qa.job[qa.count++] = qmm::I8QuantizeJob{p.x, reinterpret_cast<int8_t*>(next),
+                                                reinterpret_cast<float*>(next + up256((size_t)p.m * p.k)), p.m, p.k, p.x_type, 0};
+        next += i8_codes_bytes(p.m, p.k);
+      }
+      p.x = qa.job[job[same]].codes;
+      p.sx = qa.job[job[same]].scales;
+      p.x_type = QMM_I8;
+    }
+    if (qa.count > 0)
+      if (int st = hip_status(qmm::launch_i8_quantize(qa, (hipStream_t)stream), fn)) return st;
+  }
+  return hip_status(qmm::launch_i8_gemm(g, way, (hipStream_t)stream), fn);
 }
 
 size_t qmm_i8_grouped_workspace_size(int rows, int k, int x_type) {
@@ -922,9 +930,10 @@ static int i8_routed(const char* fn, const int8_t* w, const float* w_scales, con
   const size_t y_bytes = (size_t)pairs * n * i8_width(y_type);
   if (overlap(y, y_bytes, x, (size_t)rows * k * i8_width(x_type)))
     return fail(QMM_ERR_INVALID_ARG, "%s: the output overlaps its rows", fn);
-  qmm::I8MoeArgs g{static_cast<const int8_t*>(x), x_scales, w, w_scales, w2, w2_scales, static_cast<const int32_t*>(plan),
-                   y, t, top_k, e, n, k, per_pair, y_type, qmm::moe_plan_rows((int)pairs, e), 1};
-  if (x_type != QMM_I8) {
+  qmm::I8MoeArgs g{x, x_scales, w, w_scales, w2, w2_scales, static_cast<const int32_t*>(plan),
+                   y, t, top_k, e, n, k, per_pair, x_type, y_type, qmm::moe_plan_rows((int)pairs, e), 1};
+  const qmm::I8Way way = qmm::i8_moe_way(g);
+  if (x_type != QMM_I8 && !way.staged) {
     qmm::I8QuantizeArgs qa{};
     int8_t* codes = static_cast<int8_t*>(workspace);
     float* scales = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)rows * k));
@@ -933,8 +942,9 @@ static int i8_routed(const char* fn, const int8_t* w, const float* w_scales, con
     if (int st = hip_status(qmm::launch_i8_quantize(qa, (hipStream_t)stream), fn)) return st;
     g.x = codes;
     g.sx = scales;
+    g.x_type = QMM_I8;
   }
-  return hip_status(qmm::launch_i8_moe(g, (hipStream_t)stream), fn);
+  return hip_status(qmm::launch_i8_moe(g, way, (hipStream_t)stream), fn);
 }
 
 int qmm_i8_gemm_grouped(const int8_t* w, const float* w_scales, const void* a, const float* a_scales,

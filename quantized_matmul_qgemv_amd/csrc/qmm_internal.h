@@ -241,35 +241,42 @@ struct I8QuantizeArgs {
 hipError_t launch_i8_quantize(I8QuantizeArgs& g, hipStream_t st);
 
 struct I8Problem {
-  const int8_t* x;
-  const float* sx;
+  const void* x;    // codes, or values that the product rounds itself
+  const float* sx;  // of codes
   const int8_t* w;
   const float* sw;
   const float* bias;
   void* y;
-  int32_t m, n, k, y_type;
+  int32_t m, n, k, x_type, y_type;
   int32_t first;  // workgroup
 };
 struct I8GemmArgs {
   I8Problem p[kI8MaxProblems];
   int32_t count;
 };
-hipError_t launch_i8_gemm(I8GemmArgs& g, hipStream_t st);
+struct I8Way {
+  bool few;     // few rows: no tiles
+  bool staged;  // and x is taken as it is, the product rounds it itself
+  int shape;    // of the tiles
+};
+I8Way i8_gemm_way(const I8GemmArgs& g);
+hipError_t launch_i8_gemm(I8GemmArgs& g, I8Way way, hipStream_t st);
 
 struct I8MoeArgs {
-  const int8_t* x;
-  const float* sx;
+  const void* x;    // codes, or values that the product rounds itself
+  const float* sx;  // of codes
   const int8_t* w;
   const float* sw;
   const int8_t* w2;  // up, or null
   const float* sw2;
   const int32_t* plan;
   void* y;
-  int32_t t, top_k, e, n, k, a_row_per_pair, y_type;
+  int32_t t, top_k, e, n, k, a_row_per_pair, x_type, y_type;
   int32_t plan_rows;  // row tile of the plan
   int32_t subs;       // workgroups that share one of its row tiles
 };
-hipError_t launch_i8_moe(I8MoeArgs& g, hipStream_t st);
+I8Way i8_moe_way(const I8MoeArgs& g);
+hipError_t launch_i8_moe(I8MoeArgs& g, I8Way way, hipStream_t st);
 
 hipError_t launch_quantize(const float* w, uint32_t* words, uint16_t* s, uint16_t* b, int n,
                            int k, int bits, int group_size, hipStream_t st);

@@ -196,6 +196,34 @@ def test_given_codes_and_codes_formed_in_the_call_agree_bit_by_bit(m):
     assert torch.equal(qmm.i8_gemm(dev(w), dev(ws), x[:1].contiguous()), a[:1])
 
 
+# (m, n, k): rounded by the product with 8, 4, 2 and 1 waves a row, one batch of k and
+# several, k at the limit of what a workgroup rounds and past it; 8, 4 and 2 waves a
+# column block; codes in few rows
+FEW = [(1, 5, 16), (1, 33, 64), (1, 100, 2576), (1, 40, 16384), (1, 40, 16400), (2, 31, 8192), (2, 31, 8208), (3, 17, 4096),
+       (4, 70, 1040), (4, 70, 4112), (5, 16, 2048), (7, 15, 2064), (8, 257, 528), (8, 64, 2048), (9, 65, 512), (12, 100, 336),
+       (16, 48, 1296), (1, 16400, 144), (3, 20001, 80), (2, 33001, 272), (16, 16384, 48), (16, 16400, 48), (13, 30, 9728)]
+
+
+@pytest.mark.parametrize("xt", FLOATS + [torch.int8], ids=ids)
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_few_rows(m, n, k, xt):
+    say("i8 gemm few rows", m, n, k, xt)
+    r = np.random.default_rng([22, m, n, k])
+    w, ws = weights(r, n, k)
+    b = r.standard_normal(n).astype(np.float32)
+    y = Guarded((m, n), F32)
+    if xt == torch.int8:
+        q, s = r.integers(-128, 128, (m, k)).astype(np.int8), (r.random(m) * 0.1).astype(np.float32)
+        x, xs = dev(q), dev(s)
+    else:
+        x, xs = activations(r, m, k, xt), None
+        q, s = ref.rows_f64(f64(x))
+    qmm.i8_gemm(dev(w), dev(ws), x, xs, bias=dev(b), y=y.t)
+    torch.cuda.synchronize()
+    y.check("y")
+    ref.check(f64(y.t), ref.product_f64(q, s, w, ws, b), F32, (m, n, k))
+
+
 @pytest.mark.parametrize("m", [1, 7, 33, 300])
 def test_largest_sums_are_exact(m):
     """All codes at -128 over the longest k: 128 * 128 * 131008 is below 2^31."""

@@ -93,6 +93,27 @@ def test_gate_and_up(t, top_k, e, n, k, kind, xt, ht):
     ref.check(f64(h.t), want([gate, up], ref.rows_f64(f64(x)), I, False), ht, (t, top_k, e, n, k))
 
 
+@pytest.mark.parametrize("t,top_k,e,n,k,kind", [
+    (1, 1, 3, 20, 16, "any"), (1, 8, 128, 200, 2048, "any"), (1, 8, 9, 65, 2064, "any"), (2, 4, 5, 33, 1040, "bad"),
+    (4, 2, 2, 100, 272, "one"), (2, 8, 30, 48, 528, "any"), (4, 4, 6, 17, 4112, "few"), (16, 1, 3, 70, 96, "one"),
+    (1, 16, 2, 2100, 64, "few"), (1, 2, 4, 16500, 48, "any")])
+@pytest.mark.parametrize("xt", [F16, BF16, F32], ids=ids)
+def test_few_pairs(t, top_k, e, n, k, kind, xt):
+    """Every row of x in every type, rounded in the product and before it."""
+    test_gate_and_up(t, top_k, e, n, k, kind, xt, F32)
+    say("i8 grouped few", t, top_k, e, n, k, kind, xt)
+    r = np.random.default_rng([23, t, top_k, e, n, k])
+    w, ws = experts(r, e, n, k)
+    I = some_ids(r, t, top_k, e, kind)
+    a = activations(r, t * top_k, k, xt)
+    D = dev(I)
+    y = Guarded((t * top_k, n), F32)
+    qmm.i8_gemm_grouped(dev(w), dev(ws), a, D, qmm.moe_route(D, e), True, y=y.t)
+    torch.cuda.synchronize()
+    y.check("y")
+    ref.check(f64(y.t), want([(w, ws)], ref.rows_f64(f64(a)), I, True), F32, (t, top_k, e, n, k))
+
+
 @pytest.mark.parametrize("shape", [0, 1])
 @pytest.mark.parametrize("t,top_k,e,n,k,kind", SIZES)
 def test_both_tile_shapes(t, top_k, e, n, k, kind, shape, monkeypatch):
