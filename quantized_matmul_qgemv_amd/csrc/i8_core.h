@@ -255,7 +255,8 @@ constexpr int kI8OutRow = 144;  // bytes of a row of 128 in LDS: neighbours stan
 
 // The tile's results: scaled, rounded, and by way of LDS (32 rows of 128 bytes
 // a wave at a time) out in whole lines, columns [n0, n0 + cols) of n.
-template <class S, bool GATED>
+// SUMS: the int32 sums as they are.
+template <class S, bool GATED, bool SUMS>
 __device__ __forceinline__ void i8_finish(const i32x16 (&acc)[S::TM][S::TN], const I8Scales<S>& scales, char* lds, void* y,
                                           int type, bool biased, int n, int n0, int rows, int cols) {
   constexpr int OC = GATED ? 16 : 32;  // output columns of a block
@@ -288,7 +289,7 @@ __device__ __forceinline__ void i8_finish(const i32x16 (&acc)[S::TM][S::TN], con
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int r = lane & 31, h = lane >> 5;
   char* out = lds + FIRST + wave * 32 * kI8OutRow;
-  const int width = type == kI8F32 ? 4 : 2;
+  const int width = SUMS || type == kI8F32 ? 4 : 2;
   const int blocks = 128 / (OC * width);  // of OC columns in 128 bytes
   // whole pieces of 16 bytes where every row starts on one
   const bool wide = (size_t)n * width % 16 == 0 && ((uintptr_t)y & 15) == 0;
@@ -307,7 +308,8 @@ __device__ __forceinline__ void i8_finish(const i32x16 (&acc)[S::TM][S::TN], con
         const float4_t sw = *reinterpret_cast<const float4_t*>(ws + c0 + c);
         float4_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][4 * q + e] * sx * sw[e];
+        for (int e = 0; e < 4; ++e)
+          v[e] = SUMS ? __int_as_float(acc[i][j][4 * q + e]) : (float)acc[i][j][4 * q + e] * sx * sw[e];
         if constexpr (GATED) {
           const float4_t su = *reinterpret_cast<const float4_t*>(ws + c0 + 16 + c);
 #pragma unroll
@@ -316,7 +318,7 @@ __device__ __forceinline__ void i8_finish(const i32x16 (&acc)[S::TM][S::TN], con
           v += *reinterpret_cast<const float4_t*>(bs + c0 + c);
         }
         char* o = out + r * kI8OutRow + (place * OC + c) * width;
-        if (type == kI8F32) *reinterpret_cast<float4_t*>(o) = v;
+        if (width == 4) *reinterpret_cast<float4_t*>(o) = v;
         else *reinterpret_cast<u32x2*>(o) = u32x2{i8_pair(type, v[0], v[1]), i8_pair(type, v[2], v[3])};
       }
       if (place + 1 < blocks && j + 1 < S::TN) continue;
@@ -338,16 +340,17 @@ __device__ __forceinline__ void i8_finish(const i32x16 (&acc)[S::TM][S::TN], con
             *reinterpret_cast<u32x4*>(static_cast<char*>(y) + at * width) = v;
           }
         }
-      } else if (type == kI8F32) {
-        for (int t = 0; t < 16; ++t) {
-          const int rr = t * 2 + h;
-          if (r0 + rr < rows && r < have)
-            static_cast<float*>(y)[(size_t)ys[r0 + rr] * n + n0 + s0 + r] = *reinterpret_cast<const float*>(out + rr * kI8OutRow + r * 4);
-        }
       } else {
-        for (int t = 0; t < 32; ++t)
-          if (r0 + t < rows && lane < have)
-            static_cast<uint16_t*>(y)[(size_t)ys[r0 + t] * n + n0 + s0 + lane] = *reinterpret_cast<const uint16_t*>(out + t * kI8OutRow + lane * 2);
+        const int columns = 128 / width;
+#pragma unroll 1
+        for (int t = lane; t < 32 * columns; t += 64) {
+          const int rr = t / columns, c = t % columns;
+          if (r0 + rr >= rows || c >= have) continue;
+          const size_t at = (size_t)ys[r0 + rr] * n + n0 + s0 + c;
+          const char* from = out + rr * kI8OutRow + c * width;
+          if (width == 4) static_cast<uint32_t*>(y)[at] = *reinterpret_cast<const uint32_t*>(from);
+          else static_cast<uint16_t*>(y)[at] = *reinterpret_cast<const uint16_t*>(from);
+        }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();

@@ -93,12 +93,14 @@ hipError_t launch_i8_quantize(I8QuantizeArgs& g, hipStream_t st) {
 
 constexpr int kI8Band = 8;
 
-template <class S>
-__global__ __launch_bounds__(S::THREADS) void i8_gemm_kernel(I8GemmArgs g) {
+template <class S, bool PARTS>
+__global__ __launch_bounds__(S::THREADS) void i8_gemm_kernel(I8GemmArgs g, int splits) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   // workgroups are dealt to the 8 XCDs in turn: each XCD gets a run of tiles
-  const int each = gridDim.x / 8, more = gridDim.x % 8, xcd = blockIdx.x % 8;
+  const int all = gridDim.x, each = all / 8, more = all % 8, xcd = blockIdx.x % 8;
   int b = xcd * each + (xcd < more ? xcd : more) + blockIdx.x / 8, which = 0;
+  const int split = PARTS ? b / (all / splits) : 0;  // one part of k after the other
+  if (PARTS) b -= split * (all / splits);
   while (which + 1 < g.count && b >= g.p[which + 1].first) ++which;
   const I8Problem& p = g.p[which];
   b -= p.first;
@@ -119,34 +121,84 @@ __global__ __launch_bounds__(S::THREADS) void i8_gemm_kernel(I8GemmArgs g) {
   scales.load([&](int i) { return m0 + (i < rows ? i : rows - 1); }, [&](int, int row) { return p.sx[row]; },
               [&](int i) { return p.sw[n0 + (i < cols ? i : cols - 1)]; },
               [&](int i) { return p.bias ? p.bias[n0 + (i < cols ? i : cols - 1)] : 0.0f; });
-  i8_tile<S, false>(static_cast<const int8_t*>(p.x) + (size_t)m0 * p.k, [&](int i) { return i < rows ? i : rows - 1; }, p.w + (size_t)n0 * p.k,
-                    p.w, [&](int i) { return i < cols ? i : cols - 1; }, p.k, 0, (p.k + S::BK - 1) / S::BK, lds, acc);
-  i8_finish<S, false>(acc, scales, lds, p.y, p.y_type, p.bias != nullptr, p.n, n0, rows, cols);
+  const int steps = (p.k + S::BK - 1) / S::BK;
+  const int s0 = PARTS ? (int)((long)steps * split / splits) : 0, s1 = PARTS ? (int)((long)steps * (split + 1) / splits) : steps;
+  i8_tile<S, false>(static_cast<const int8_t*>(p.x) + (size_t)m0 * p.k, [&](int i) { return i < rows ? i : rows - 1; },
+                    p.w + (size_t)n0 * p.k, p.w, [&](int i) { return i < cols ? i : cols - 1; }, p.k, s0, s1, lds, acc);
+  void* y = PARTS ? static_cast<void*>(p.sums + (size_t)split * p.m * p.n) : p.y;
+  i8_finish<S, false, PARTS>(acc, scales, lds, y, p.y_type, !PARTS && p.bias != nullptr, p.n, n0, rows, cols);
+}
+
+// The sums of the parts of k, scaled and rounded: V neighbouring columns a thread.
+template <int V>
+__global__ __launch_bounds__(256) void i8_sum_kernel(I8GemmArgs g, int splits) {
+  int b = blockIdx.x, which = 0;
+  while (which + 1 < g.count && b >= g.p[which + 1].first) ++which;
+  const I8Problem& p = g.p[which];
+  const long at = ((long)(b - p.first) * 256 + threadIdx.x) * V, outputs = (long)p.m * p.n;
+  if (at >= outputs) return;
+  const int row = (int)(at / p.n), c = (int)(at % p.n);
+  typedef int32_t vec __attribute__((ext_vector_type(V)));
+  vec sum = *reinterpret_cast<const vec*>(p.sums + at);
+  for (int i = 1; i < splits; ++i) sum += *reinterpret_cast<const vec*>(p.sums + at + i * outputs);
+  const float sx = p.sx[row];
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = (float)sum[i] * sx * p.sw[c + i];
+    if (p.bias) v[i] += p.bias[c + i];
+  }
+  if (p.y_type == kI8F32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) static_cast<float*>(p.y)[at + i] = v[i];
+  } else {
+    uint16_t* y = static_cast<uint16_t*>(p.y) + at;
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = (uint16_t)i8_pair(p.y_type, v[i], v[i]);
+  }
+}
+
+static hipError_t launch_sum(I8GemmArgs& g, int splits, hipStream_t st) {
+  bool four = true;
+  for (int i = 0; i < g.count; ++i) four = four && g.p[i].n % 4 == 0;
+  long blocks = 0;
+  for (int i = 0; i < g.count; ++i) {
+    g.p[i].first = (int)blocks;
+    blocks += ((long)g.p[i].m * g.p[i].n / (four ? 4 : 1) + 255) / 256;
+  }
+  if (four) hipLaunchKernelGGL((i8_sum_kernel<4>), dim3((unsigned)blocks), dim3(256), 0, st, g, splits);
+  else hipLaunchKernelGGL((i8_sum_kernel<1>), dim3((unsigned)blocks), dim3(256), 0, st, g, splits);
+  return hipGetLastError();
 }
 
 template <class S>
-static hipError_t launch_shape(I8GemmArgs& g, hipStream_t st) {
+static hipError_t launch_shape(I8GemmArgs& g, int splits, hipStream_t st) {
   long tiles = 0;
   for (int i = 0; i < g.count; ++i) {
     g.p[i].first = (int)tiles;
     tiles += (long)((g.p[i].m + S::BM - 1) / S::BM) * ((g.p[i].n + S::BN - 1) / S::BN);
   }
   if (tiles == 0) return hipSuccess;
-  hipLaunchKernelGGL((i8_gemm_kernel<S>), dim3((unsigned)tiles), dim3(S::THREADS), 0, st, g);
-  return hipGetLastError();
+  if (splits == 1) {
+    hipLaunchKernelGGL((i8_gemm_kernel<S, false>), dim3((unsigned)tiles), dim3(S::THREADS), 0, st, g, 1);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((i8_gemm_kernel<S, true>), dim3((unsigned)(tiles * splits)), dim3(S::THREADS), 0, st, g, splits);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess ? err : launch_sum(g, splits, st);
 }
 
-// Tile shapes and what a tile costs alone on its CU (shapes of 160 KB / LDS > 1:
-// with that many beside it): `fixed` us and `step` us for 128 bytes of k.  Measured on
-// products with cold weights (m x n x k, us with about 4 us of launch):
-//   shape        512x2560x4096  512x9728x2560  1024x9728x2560  2048x2560x9728  2048x9728x2560  16384x2560x9728
-//   64 x 64               22.9           35.1            58.8            97.1             103              692
-//   64 x 128              19.9           41.1            64.5           101.8             123                -
-//   128 x 128             24.4           38.4            54.9            94.2              87              456
-//   128 x 192             29.0           25.7            47.0            62.6              81                -
-//   256 x 192             45.7           38.8            39.6           102.9              74              432
-//   256 x 256             54.8           44.7            45.1           123.0              80              403
-//   256 x 320             62.6           49.2            49.7           137.1              57              349
+// Tile shapes and what a round of their tiles costs on a full chip (of shapes that a
+// CU holds several of: of all it holds): `fixed` us and `step` us for 128 bytes of k.
+// Measured, k in one part (m x n x k, us of a call of codes, graph, cold weights):
+//   shape      64x1024x4096  512x2560x4096  512x9728x2560  1024x2560x9728  2048x2560x9728  2048x9728x2560  16384x2560x9728
+//   64 x 64            11.2           13.9           31.7            58.5            94.7           101.1              649
+//   64 x 128           13.6           14.1           38.2            67.3           102.7           121.9              632
+//   128 x 128          18.3           18.5           35.5            47.3            92.9            86.3              485
+//   128 x 192          24.2           24.9           23.8            57.0            67.0            83.2              465
+//   256 x 192          37.9           39.1           35.0            93.7            93.8            72.0              420
+//   256 x 256          44.3           48.5           39.8           110.9           111.0            79.2              385
+//   256 x 320          56.8           57.9           44.9           129.5           130.2            58.2              346
 // A larger tile moves fewer bytes for its products; which one is best is mostly a
 // matter of how evenly its tiles fall on the 256 CUs.
 struct I8Choice {
@@ -154,14 +206,29 @@ struct I8Choice {
   float fixed, step;
 };
 constexpr I8Choice kI8Choices[] = {
-    {64, 64, 3, 3.0f, 0.55f},  {64, 128, 1, 3.0f, 0.45f},  {128, 128, 1, 4.0f, 0.60f}, {128, 192, 1, 5.0f, 0.75f},
-    {256, 192, 1, 7.0f, 1.25f}, {256, 256, 1, 8.0f, 1.52f}, {256, 320, 1, 9.0f, 1.72f},
+    {64, 64, 3, 3.0f, 0.70f},  {64, 128, 1, 3.5f, 0.42f},  {128, 128, 1, 5.0f, 0.55f}, {128, 192, 1, 4.0f, 0.78f},
+    {256, 192, 1, 7.0f, 1.30f}, {256, 256, 1, 8.0f, 1.65f}, {256, 320, 1, 9.0f, 2.10f},
 };
 constexpr int kI8Shapes = sizeof(kI8Choices) / sizeof(kI8Choices[0]);
 
-static int i8_choose(const I8GemmArgs& g) {
-  int best = 0;
+// Parts of k, where there are too few tiles for the CUs: the sums of each part go
+// through memory (int32, so that their order does not matter) and a second launch adds
+// them up: `kI8SumFixed` us and 8 bytes an output and part at 4 TB/s.  64 x 2560 x
+// 9728: 31.1 us in one part, 14.5 in six; 64 x 1024 x 4096: 11.2, 9.0 in four.
+constexpr float kI8SumFixed = 4.0f, kI8SumRate = 4.0e6f;
+constexpr long kI8SumMost = 64l << 20;  // bytes of sums
+
+static void i8_choose(const I8GemmArgs& g, I8Way& way) {
+  const int forced = way.shape;
   double least = 1e30;
+  double outputs = 0;
+  int fewest = 1 << 30;
+  for (int i = 0; i < g.count; ++i) {
+    const int steps = (g.p[i].k + 127) / 128;
+    fewest = steps < fewest ? steps : fewest;
+    outputs += (double)g.p[i].m * g.p[i].n;
+  }
+  const char* force = getenv("QMM_I8_SPLITS");  // tuning sweeps and tests
   for (int c = 0; c < kI8Shapes; ++c) {
     const I8Choice& h = kI8Choices[c];
     double tiles = 0, steps = 0;
@@ -170,17 +237,24 @@ static int i8_choose(const I8GemmArgs& g) {
       tiles += t;
       steps += t * ((g.p[i].k + 127) / 128);
     }
+    if (forced >= 0 && c != forced) continue;
     const double slots = 256.0 * h.at_once;
-    const double rounds = (double)(long)((tiles + slots - 1) / slots);
-    // fewer tiles than places: they share a CU with fewer others
-    const double share = tiles < slots && h.at_once > 1 ? 0.5 + 0.5 * tiles / slots : 1.0;
-    const double cost = rounds * (h.fixed + h.step * share * steps / tiles);
-    if (cost < least) {
-      least = cost;
-      best = c;
+    for (int splits = 1; splits <= 16 && splits <= fewest; ++splits) {
+      if (splits > 1 && (tiles * splits > slots || outputs * splits * 4 > kI8SumMost)) break;
+      if (force != nullptr && atoi(force) > 0 && atoi(force) <= fewest && splits != atoi(force)) continue;
+      const double parts = tiles * splits;
+      // whole rounds; where a CU holds several, its share of one
+      const double full = (double)(long)((parts + slots - 1) / slots);
+      const double share = parts / 256 > 1 ? parts / slots : 1.0 / h.at_once;
+      double cost = (h.at_once > 1 ? share : full) * h.step * steps / parts + full * h.fixed;
+      if (splits > 1) cost += kI8SumFixed + outputs * splits * 8 / kI8SumRate;
+      if (cost < least) {
+        least = cost;
+        way.shape = c;
+        way.splits = splits;
+      }
     }
   }
-  return best;
 }
 
 template <int U, bool LOOP, int TYPE>
@@ -240,11 +314,13 @@ static hipError_t launch_few(I8GemmArgs& g, hipStream_t st) {
 //    8 x 151936 x 1024              34.6                 41.4              38.2
 //   16 x 9728 x 2560                   -                 16.4              17.5
 //   16 x 151936 x 1024                 -                 46.9              39.4
+// (The workspace's size follows from it: it looks at m, n, k and x's type alone.)
 I8Way i8_gemm_way(const I8GemmArgs& g) {
-  I8Way way{false, false, 0};
+  I8Way way{false, false, -1, 1};
   const char* force = getenv("QMM_I8_FORCE");  // tuning sweeps and tests: a tile shape by its place
   if (force != nullptr && atoi(force) >= 0 && atoi(force) < kI8Shapes) {
     way.shape = atoi(force);
+    i8_choose(g, way);
     return way;
   }
   int most = 0;
@@ -254,7 +330,7 @@ I8Way i8_gemm_way(const I8GemmArgs& g) {
     if (g.p[i].x_type == kI8Codes || g.p[i].x_type != g.p[0].x_type || !i8_can_stage(g.p[i].m, g.p[i].k)) way.staged = false;
   }
   way.few = way.staged || (most <= kI8FewRows && i8_blocks(g) <= 1024);
-  if (!way.few) way.shape = i8_choose(g);
+  if (!way.few) i8_choose(g, way);
   return way;
 }
 
@@ -266,13 +342,13 @@ hipError_t launch_i8_gemm(I8GemmArgs& g, I8Way way, hipStream_t st) {
     default: return launch_few<kI8Codes>(g, st);
   }
   switch (way.shape) {
-    case 0: return launch_shape<I8Shape<64, 64, 2, 2, 3, 128>>(g, st);
-    case 1: return launch_shape<I8Shape<64, 128, 2, 4, 6, 128>>(g, st);
-    case 2: return launch_shape<I8Shape<128, 128, 2, 4, 3, 128>>(g, st);
-    case 3: return launch_shape<I8Shape<128, 192, 4, 2, 3, 128>>(g, st);
-    case 4: return launch_shape<I8Shape<256, 192, 4, 2, 2, 128>>(g, st);
-    case 5: return launch_shape<I8Shape<256, 256, 2, 4, 2, 128>>(g, st);
-    default: return launch_shape<I8Shape<256, 320, 4, 2, 2, 128>>(g, st);
+    case 0: return launch_shape<I8Shape<64, 64, 2, 2, 3, 128>>(g, way.splits, st);
+    case 1: return launch_shape<I8Shape<64, 128, 2, 4, 6, 128>>(g, way.splits, st);
+    case 2: return launch_shape<I8Shape<128, 128, 2, 4, 3, 128>>(g, way.splits, st);
+    case 3: return launch_shape<I8Shape<128, 192, 4, 2, 3, 128>>(g, way.splits, st);
+    case 4: return launch_shape<I8Shape<256, 192, 4, 2, 2, 128>>(g, way.splits, st);
+    case 5: return launch_shape<I8Shape<256, 256, 2, 4, 2, 128>>(g, way.splits, st);
+    default: return launch_shape<I8Shape<256, 320, 4, 2, 2, 128>>(g, way.splits, st);
   }
 }
 

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
               [](int) { return 0.0f; });
   i8_tile<S, GATED>(static_cast<const int8_t*>(g.x), [&](int i) { return row(pair(i)); }, g.w + at, GATED ? g.w2 + at : g.w + at,
                     [&](int i) { return i < cols ? i : cols - 1; }, g.k, 0, (g.k + S::BK - 1) / S::BK, lds, acc);
-  i8_finish<S, GATED>(acc, scales, lds, g.y, g.y_type, false, g.n, n0, mt.rows, cols);
+  i8_finish<S, GATED, false>(acc, scales, lds, g.y, g.y_type, false, g.n, n0, mt.rows, cols);
 }
 
 template <class S, bool GATED>
@@ -172,7 +172,7 @@ static hipError_t launch_moe_few_type(I8MoeArgs& g, hipStream_t st) {
 // 128 experts, gate and up of 768 x 2048: 9.7 us, as codes 13.4, in tiles 29.6.
 I8Way i8_moe_way(const I8MoeArgs& g) {
   const long pairs = (long)g.t * g.top_k;
-  I8Way way{pairs <= kI8FewRows, false, g.plan_rows >= 128 ? 1 : 0};
+  I8Way way{pairs <= kI8FewRows, false, g.plan_rows >= 128 ? 1 : 0, 1};
   if (const char* env = getenv("QMM_I8_MOE_FORCE")) {  // tuning sweeps and tests
     way.few = false;
     way.shape = atoi(env) != 0;

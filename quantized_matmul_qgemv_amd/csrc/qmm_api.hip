@@ -789,15 +789,33 @@ int qmm_i8_quantize(const void* x, int x_type, int8_t* codes, float* scales, int
   return hip_status(qmm::launch_i8_quantize(q, (hipStream_t)stream), fn);
 }
 
-size_t qmm_i8_gemm_workspace_size(const qmm_i8_problem* problems, int count) {
-  if (problems == nullptr || count < 1 || count > qmm::kI8MaxProblems) return 0;
+// What a call of these problems keeps in its workspace: the codes of the x that it
+// rounds beforehand, then the sums of the parts of k.
+static size_t i8_workspace(const qmm_i8_problem* problems, int count, const qmm::I8GemmArgs& g, const qmm::I8Way& way) {
   size_t need = 0;
   for (int i = 0; i < count; ++i) {
     const qmm_i8_problem& q = problems[i];
-    if (q.m < 0 || q.m > kMaxI8Rows || q.n < 1 || q.n > kMaxI8N || !i8_k(q.k) || !i8_x_type(q.x_type)) return 0;
-    if (q.x_type != QMM_I8 && i8_first_of(problems, i) == i) need += i8_codes_bytes(q.m, q.k);
+    if (q.m > 0 && q.x_type != QMM_I8 && !way.staged && i8_first_of(problems, i) == i) need += i8_codes_bytes(q.m, q.k);
   }
+  if (way.splits > 1)
+    for (int i = 0; i < g.count; ++i) need += up256((size_t)way.splits * g.p[i].m * g.p[i].n * 4);
   return need;
+}
+
+size_t qmm_i8_gemm_workspace_size(const qmm_i8_problem* problems, int count) {
+  if (problems == nullptr || count < 1 || count > qmm::kI8MaxProblems) return 0;
+  qmm::I8GemmArgs g{};
+  for (int i = 0; i < count; ++i) {
+    const qmm_i8_problem& q = problems[i];
+    if (q.m < 0 || q.m > kMaxI8Rows || q.n < 1 || q.n > kMaxI8N || !i8_k(q.k) || !i8_x_type(q.x_type)) return 0;
+    if (q.m == 0) continue;
+    qmm::I8Problem& p = g.p[g.count++];
+    p.m = q.m;
+    p.n = q.n;
+    p.k = q.k;
+    p.x_type = q.x_type;
+  }
+  return g.count == 0 ? 0 : i8_workspace(problems, count, g, qmm::i8_gemm_way(g));
 }
 
 int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size_t workspace_bytes,
@@ -845,25 +863,25 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
       if (what) return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: y overlaps the %s of problem %d", fn, i, what, j);
     }
   }
-  const size_t need = qmm_i8_gemm_workspace_size(problems, count);
-  if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need)
-      return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
-    CHECK_PTR(workspace, 16);
-  }
   qmm::I8GemmArgs g{};
   int from[qmm::kI8MaxProblems];  // the problem that a place of g came from
   for (int i = 0; i < count; ++i) {
     const qmm_i8_problem& q = problems[i];
     if (q.m == 0) continue;
     from[g.count] = i;
-    g.p[g.count++] = qmm::I8Problem{q.x, q.x_scales, q.w, q.w_scales, q.bias, q.y, q.m, q.n, q.k, q.x_type, q.y_type, 0};
+    g.p[g.count++] = qmm::I8Problem{q.x, q.x_scales, q.w, q.w_scales, q.bias, q.y, q.m, q.n, q.k, q.x_type, q.y_type, 0, nullptr};
   }
   if (g.count == 0) return QMM_OK;
   const qmm::I8Way way = qmm::i8_gemm_way(g);
+  const size_t need = i8_workspace(problems, count, g, way);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
+    CHECK_PTR(workspace, 16);
+  }
+  char* next = static_cast<char*>(workspace);
   if (!way.staged) {
     qmm::I8QuantizeArgs qa{};
-    char* next = static_cast<char*>(workspace);
     int job[qmm::kI8MaxProblems];  // of a problem's x
     for (int i = 0; i < g.count; ++i) {
       qmm::I8Problem& p = g.p[i];
@@ -882,6 +900,11 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
     if (qa.count > 0)
       if (int st = hip_status(qmm::launch_i8_quantize(qa, (hipStream_t)stream), fn)) return st;
   }
+  if (way.splits > 1)
+    for (int i = 0; i < g.count; ++i) {
+      g.p[i].sums = reinterpret_cast<int32_t*>(next);
+      next += up256((size_t)way.splits * g.p[i].m * g.p[i].n * 4);
+    }
   return hip_status(qmm::launch_i8_gemm(g, way, (hipStream_t)stream), fn);
 }
 

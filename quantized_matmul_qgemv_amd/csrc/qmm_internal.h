@@ -249,6 +249,7 @@ struct I8Problem {
   void* y;
   int32_t m, n, k, x_type, y_type;
   int32_t first;  // workgroup
+  int32_t* sums;  // [splits][m][n], where k is split
 };
 struct I8GemmArgs {
   I8Problem p[kI8MaxProblems];
@@ -258,6 +259,7 @@ struct I8Way {
   bool few;     // few rows: no tiles
   bool staged;  // and x is taken as it is, the product rounds it itself
   int shape;    // of the tiles
+  int splits;   // parts of k, summed by a launch of their own (1: none)
 };
 I8Way i8_gemm_way(const I8GemmArgs& g);
 hipError_t launch_i8_gemm(I8GemmArgs& g, I8Way way, hipStream_t st);

@@ -130,6 +130,38 @@ def test_products_by_every_tile_shape(m, n, k, shape, monkeypatch):
     codes_case(m, n, k)
 
 
+@pytest.mark.parametrize("splits", [2, 3, 8])
+@pytest.mark.parametrize("shape", range(SHAPES))
+def test_k_in_parts_gives_the_same_bits(shape, splits, monkeypatch):
+    """Several products of a call, of odd and even widths, each k in parts."""
+    say("i8 gemm parts", shape, splits)
+    r = np.random.default_rng([24, shape, splits])
+    for ns in ((100, 36, 260), (33, 130)):
+        for yt in FLOATS:
+            x = activations(r, 70, 1296, F16)
+            monkeypatch.setenv("QMM_I8_FORCE", str(shape))
+            monkeypatch.setenv("QMM_I8_SPLITS", str(splits))
+            problems, wants = [], []
+            for i, n in enumerate(ns):
+                w, ws = weights(r, n, 1296)
+                b = r.standard_normal(n).astype(np.float32) if i != 1 else None
+                problems.append((dev(w), dev(ws), x, None, None if b is None else dev(b), Guarded((70, n), yt)))
+                wants.append(ref.product_f64(*ref.rows_f64(f64(x)), w, ws, b))
+            given = [p[:5] + (p[5].t,) for p in problems]
+            wsp = qmm.i8_gemm_workspace(given)
+            assert wsp.numel() >= splits * 70 * sum(ns) * 4
+            guarded = Guarded((wsp.numel(),), torch.uint8)
+            qmm.i8_gemm_batched(given, workspace=guarded.t)
+            torch.cuda.synchronize()
+            guarded.check("workspace")
+            for p, want in zip(problems, wants):
+                p[5].check("y")
+                ref.check(f64(p[5].t), want, yt, (shape, splits))
+            monkeypatch.setenv("QMM_I8_SPLITS", "1")
+            for p, y in zip(problems, qmm.i8_gemm_batched([p[:5] + (None,) for p in problems], dtype=yt)):
+                assert torch.equal(y, p[5].t)
+
+
 @pytest.mark.parametrize("shape", range(SHAPES))
 @pytest.mark.parametrize("yt", FLOATS, ids=ids)
 def test_outputs_of_every_type_by_every_tile_shape(yt, shape, monkeypatch):

@@ -11,7 +11,7 @@ from quantized_matmul_qgemv_amd._lib import I8Problem  # noqa: E402
 INV, UNS, WSP = _lib.QMM_ERR_INVALID_ARG, _lib.QMM_ERR_UNSUPPORTED, _lib.QMM_ERR_WORKSPACE
 F32, F16, BF16, I8 = _lib.QMM_F32, _lib.QMM_F16, _lib.QMM_BF16, _lib.QMM_I8
 A, X, Y = 0x100000, 0x80000000, 0x40000000  # fake, aligned, never dereferenced device addresses
-M, N, K = 4, 64, 64
+M, N, K = 20, 64, 64  # more rows than the product rounds itself
 
 
 def problem(**kw):
@@ -54,7 +54,7 @@ def call(problems=None, count=None, ws=A, ws_bytes=1 << 40, **kw):
     (dict(y=Y + 2), INV, "y is not 4-byte aligned"),
     (dict(y=Y + 1, y_type=F16), INV, "y is not 2-byte aligned"),
     (dict(ws=None), WSP, "workspace of 0 bytes"),
-    (dict(ws_bytes=511), WSP, "workspace of 511 bytes, 512 needed"),
+    (dict(ws_bytes=1535), WSP, "workspace of 1535 bytes, 1536 needed"),
     (dict(ws=A + 8), INV, "workspace is not 16-byte aligned"),
 ])
 def test_refusals(kw, status, text):
@@ -99,11 +99,17 @@ def size(*ps):
 def test_workspace_sizes():
     assert call(m=0) == 0  # clears the message
     one = size(problem())
-    assert one == 512  # 256 codes, four scales on 256
+    assert one == 1536  # 20 x 64 codes, 20 scales, each on 256
     assert size(problem(), problem(n=9, w=None, y=None)) == one  # one x, rounded once
-    assert size(problem(), problem(x=X + 1024)) == 2 * one
+    assert size(problem(), problem(x=X + 4096)) == 2 * one
     assert size(problem(), problem(m=M - 1)) > one
+    assert size(problem(), problem(m=0)) == one
     assert size(problem(x_type=I8)) == 0
+    assert size(problem(m=2)) == 0  # rounded by the product
+    assert size(problem(m=2), problem(m=2, x_type=BF16)) == 4 * 256  # of two types: before it
+    # k in parts: int32 sums of each part
+    parts = size(problem(x_type=I8, n=1024, k=8192))
+    assert parts >= 2 * M * 1024 * 4 and parts % (M * 1024 * 4) == 0
     for bad in (dict(k=0), dict(k=17), dict(n=0), dict(m=-1), dict(x_type=7)):
         assert size(problem(**bad)) == 0
         assert _lib.last_error() == ""
