@@ -417,8 +417,8 @@ int qmm_lora(const qmm_lora_problem* problems, int count, const int32_t* adapter
  * that holds a NaN or an infinity has scale NaN and codes 0, and so a row of
  * NaN in y.  Given codes may be anything from -128 to 127.
  *   types  QMM_F32, QMM_F16, QMM_BF16 (bit patterns); QMM_I8: codes, with their scales
- *   sizes  k a multiple of 16 up to 131008; n in [1, 2097152]; m in [0, 16777215];
- *          together the outputs of a call at most 2^35
+ *   sizes  k a multiple of 16 up to 131008; n in [1, 2097152]; m in [0, 16777215],
+ *          also over all problems of a call; the outputs of a call at most 2^35
  *   w, x, codes and workspaces 16-byte aligned, scales and bias 4-byte, y by
  *   its type (on 16 bytes, with n a multiple of 4, it is stored by whole pieces)
  * Errors of all: INVALID_ARG, UNSUPPORTED (type), WORKSPACE, HIP. */
@@ -441,7 +441,7 @@ int qmm_i8_quantize(const void* x, int x_type, int8_t* codes, float* scales, int
  * problems are read; 0 for sizes that are refused, and where none is needed:
  * then it may be NULL), contents on entry do not matter; calls (and captured
  * graphs) that share one must not run concurrently.  m = 0: the problem does
- * nothing.  One to three launches, by sizes and types. */
+ * nothing.  One to three launches, by sizes (one more for each further type of x). */
 typedef struct {
   const int8_t* w;
   const float* w_scales;

@@ -19,12 +19,12 @@ constexpr int kI8FewThreads = 64 * kI8FewWaves;
 constexpr int kI8FewRows = 16;      // rows of a workgroup: those of one operand
 constexpr int kI8FewHead = 256;     // bytes of LDS: scales of the rows, the waves' maxima
 constexpr int kI8StageRows = 8;     // rows that a workgroup can round
-constexpr int kI8StageHold = 2;     // times 16 values a lane
+constexpr int kI8StageHold = 32;    // values of a row a lane
 
 // Waves that share a row when m rows are rounded by eight.
 __host__ __device__ inline int i8_stage_group(int m) { return m == 1 ? 8 : m == 2 ? 4 : m <= 4 ? 2 : 1; }
 inline bool i8_can_stage(int m, int k) {
-  return m <= kI8StageRows && k <= 16 * 64 * kI8StageHold * i8_stage_group(m);
+  return m <= kI8StageRows && k <= 64 * kI8StageHold * i8_stage_group(m);
 }
 
 template <bool GATED>
@@ -38,31 +38,6 @@ size_t i8_few_lds(int rows, int k) {
   const size_t sums = i8_few_sums<GATED>();
   return kI8FewHead + (held > sums ? held : sums);
 }
-
-// Sixteen values as they are, and as numbers.
-template <int TYPE>
-struct I8Raw {
-  static constexpr int N = TYPE == kI8F32 ? 4 : 2;
-  u32x4 u[N];
-  __device__ __forceinline__ void load(const void* x, size_t at) {
-    auto p = (gptr<u32x4>)((gptr<char>)x + at * (TYPE == kI8F32 ? 4 : 2));
-#pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = p[i];
-  }
-  __device__ __forceinline__ void get(float (&v)[16]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (TYPE == kI8F32) {
-          v[4 * i + j] = __uint_as_float(u[i][j]);
-        } else {
-          v[8 * i + 2 * j] = TYPE == kI8F16 ? f16_bits_to_f32((uint16_t)u[i][j]) : __uint_as_float(u[i][j] << 16);
-          v[8 * i + 2 * j + 1] = TYPE == kI8F16 ? f16_bits_to_f32((uint16_t)(u[i][j] >> 16)) : __uint_as_float(u[i][j] & 0xFFFF0000u);
-        }
-      }
-  }
-};
 
 // Waves that share 16 columns: enough for about 4096 waves in all.  us of a call
 // with 8 / 4 / 2 (graph, cold weights, fp16 x): one row, 9728 x 2560: 9.6 / 12.6 /
@@ -104,17 +79,16 @@ __device__ __forceinline__ void i8_few(const I8FewTile& t, char* lds, XRow x_row
   const int end = s + each < slices ? s + each : slices;
 
   // x's rows, as they are
-  I8Raw<STAGED ? TYPE : kI8F16> raw[kI8StageHold];
+  using Raw = I8Raw<STAGED ? TYPE : kI8F32>;
+  constexpr int HOLD = STAGED ? kI8StageHold / Raw::V : 1;
+  Raw raw[HOLD];
   const int group = STAGED ? i8_stage_group(t.rows) : 8;
-  const int place = wave % group * 64 + lane, span = 64 * group;
+  const int place = (wave % group * 64 + lane) * Raw::V, span = 64 * group * Raw::V;
   const bool mine = STAGED && wave / group < t.rows;
   if constexpr (STAGED) {
     const size_t at = (size_t)x_row(mine ? wave / group : 0) * k;
 #pragma unroll
-    for (int i = 0; i < kI8StageHold; ++i) {
-      const int c = (place + i * span) * 16;
-      raw[i].load(t.x, at + (c < k ? c : 0));
-    }
+    for (int i = 0; i < HOLD; ++i) raw[i].load(t.x, at + (place + i * span < k ? place + i * span : 0));
   } else if ((int)threadIdx.x < t.rows) {
     sx[threadIdx.x] = t.sx[x_row(threadIdx.x)];
   }
@@ -192,13 +166,8 @@ __device__ __forceinline__ void i8_few(const I8FewTile& t, char* lds, XRow x_row
   if constexpr (STAGED) {
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kI8StageHold; ++i)
-      if ((place + i * span) * 16 < k) {
-        float v[16];
-        raw[i].get(v);
-        top = i8_top(v, top);
-      }
-    top = wave_umax(top);
+    for (int i = 0; i < HOLD; ++i) raw[i].top(top);
+    top = wave_umax(Raw::top_bits(top));
     if (group > 1) {  // the same in every wave
       if (lane == 0) tops[wave] = top;
       __syncthreads();
@@ -212,17 +181,10 @@ __device__ __forceinline__ void i8_few(const I8FewTile& t, char* lds, XRow x_row
     if (mine) {
       const int r = wave / group;
       if (place == 0) sx[r] = scale;
-      const bool some = scale > 0.0f;
-      const float inv = some ? 1.0f / scale : 0.0f;
+      const float inv = scale > 0.0f ? 1.0f / scale : 0.0f;
 #pragma unroll
-      for (int i = 0; i < kI8StageHold; ++i) {
-        const int c = (place + i * span) * 16;
-        if (c < k) {
-          float v[16];
-          raw[i].get(v);
-          *reinterpret_cast<i32x4*>(body + r * (k + 16) + c) = some ? i8_round16(v, scale, inv) : i32x4{0, 0, 0, 0};
-        }
-      }
+      for (int i = 0; i < HOLD; ++i)
+        if (place + i * span < k) i8_put<TYPE>(body + r * (k + 16) + place + i * span, raw[i], scale, inv);
     }
     __syncthreads();
   }

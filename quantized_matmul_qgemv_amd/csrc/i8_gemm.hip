@@ -10,16 +10,15 @@
 namespace qmm {
 
 // ---------------------------------------------------------------- rounding
-// Sixteen values a lane: one 16-byte store of codes, two (16-bit x) or four
-// (fp32 x) 16-byte loads.  A row is taken by WPR waves, which hold it in registers
-// up to 16 * 64 * WPR * R values; what is longer is read a second time.
+// A row is taken by WPR waves (1 or 4), which hold it in registers up to 16 R bytes a
+// lane; what is longer is read a second time.
 
 constexpr int kI8RoundThreads = 256;
 
-// WPR waves a row (1 or 4), R chunks of 16 values a lane held.
-template <int WPR, int R>
+template <int TYPE, int WPR, int R>
 __global__ __launch_bounds__(kI8RoundThreads) void i8_quantize_kernel(I8QuantizeArgs g) {
   __shared__ uint32_t tops[4];
+  using Raw = I8Raw<TYPE>;
   int b = blockIdx.x, job = 0;
   while (job + 1 < g.count && b >= g.job[job + 1].first) ++job;
   const I8QuantizeJob& jb = g.job[job];
@@ -28,26 +27,21 @@ __global__ __launch_bounds__(kI8RoundThreads) void i8_quantize_kernel(I8Quantize
   const int wave = threadIdx.x >> 6;
   const int row = WPR == 1 ? b * 4 + wave : b;
   if (row >= jb.m) return;  // whole waves; with WPR = 4 whole workgroups
-  const int place = WPR == 1 ? lane : threadIdx.x;
-  constexpr int SPAN = 64 * WPR;
-  const int chunks = jb.k / 16;
-  const size_t at = (size_t)row * jb.k;
-  float v[R][16];
+  const int place = (WPR == 1 ? lane : threadIdx.x) * Raw::V, k = jb.k;
+  constexpr int SPAN = 64 * WPR * Raw::V;
+  const size_t at = (size_t)row * k;
+  Raw raw[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) raw[i].load(jb.x, at + (place + i * SPAN < k ? place + i * SPAN : 0));  // the first again changes no maximum
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int c = place + i * SPAN;
-    if (c < chunks) i8_load16(jb.x, at + (size_t)c * 16, jb.type, v[i]);
+  for (int i = 0; i < R; ++i) raw[i].top(top);
+  for (int c = place + R * SPAN; c < k; c += SPAN) {
+    Raw more;
+    more.load(jb.x, at + c);
+    more.top(top);
   }
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (place + i * SPAN < chunks) top = i8_top(v[i], top);
-  for (int c = place + R * SPAN; c < chunks; c += SPAN) {
-    float u[16];
-    i8_load16(jb.x, at + (size_t)c * 16, jb.type, u);
-    top = i8_top(u, top);
-  }
-  top = wave_umax(top);
+  top = wave_umax(Raw::top_bits(top));
   if constexpr (WPR > 1) {
     if (lane == 0) tops[wave] = top;
     __syncthreads();
@@ -56,37 +50,55 @@ __global__ __launch_bounds__(kI8RoundThreads) void i8_quantize_kernel(I8Quantize
   }
   const float s = i8_scale(top);
   if (place == 0) jb.scales[row] = s;
-  const bool some = s > 0.0f;
-  const float inv = some ? 1.0f / s : 0.0f;
-  auto store = [&](int c, const float (&u)[16]) {
-    i32x4 q = some ? i8_round16(u, s, inv) : i32x4{0, 0, 0, 0};
-    *reinterpret_cast<i32x4*>(jb.codes + at + (size_t)c * 16) = q;
-  };
+  const float inv = s > 0.0f ? 1.0f / s : 0.0f;
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    if (place + i * SPAN < chunks) store(place + i * SPAN, v[i]);
-  for (int c = place + R * SPAN; c < chunks; c += SPAN) {
-    float u[16];
-    i8_load16(jb.x, at + (size_t)c * 16, jb.type, u);
-    store(c, u);
+    if (place + i * SPAN < k) i8_put<TYPE>(jb.codes + at + place + i * SPAN, raw[i], s, inv);
+  for (int c = place + R * SPAN; c < k; c += SPAN) {
+    Raw more;
+    more.load(jb.x, at + c);
+    i8_put<TYPE>(jb.codes + at + c, more, s, inv);
   }
 }
 
-hipError_t launch_i8_quantize(I8QuantizeArgs& g, hipStream_t st) {
-  // one wave a row where the row fits its registers
-  long most = 0;
-  for (int i = 0; i < g.count; ++i) most = g.job[i].k > most ? g.job[i].k : most;
-  const int wpr = most <= 4096 ? 1 : 4;
+template <int TYPE, int WPR, int R>
+static hipError_t launch_quantize_kernel(I8QuantizeArgs& g, hipStream_t st) {
   long blocks = 0;
   for (int i = 0; i < g.count; ++i) {
     g.job[i].first = (int)blocks;
-    blocks += wpr == 1 ? (g.job[i].m + 3) / 4 : g.job[i].m;
+    blocks += WPR == 1 ? (g.job[i].m + 3) / 4 : g.job[i].m;
   }
   if (blocks == 0) return hipSuccess;
-  if (wpr == 1 && most <= 1024) hipLaunchKernelGGL((i8_quantize_kernel<1, 1>), dim3(blocks), dim3(kI8RoundThreads), 0, st, g);
-  else if (wpr == 1) hipLaunchKernelGGL((i8_quantize_kernel<1, 4>), dim3(blocks), dim3(kI8RoundThreads), 0, st, g);
-  else hipLaunchKernelGGL((i8_quantize_kernel<4, 4>), dim3(blocks), dim3(kI8RoundThreads), 0, st, g);
+  hipLaunchKernelGGL((i8_quantize_kernel<TYPE, WPR, R>), dim3((unsigned)blocks), dim3(kI8RoundThreads), 0, st, g);
   return hipGetLastError();
+}
+
+// One wave a row where it holds the row and there are rows enough to fill the chip,
+// four otherwise; two pieces a lane where that is enough.
+template <int TYPE>
+static hipError_t launch_quantize_type(I8QuantizeArgs& g, hipStream_t st) {
+  constexpr int V = I8Raw<TYPE>::V;
+  long most = 0, rows = 0;
+  for (int i = 0; i < g.count; ++i) {
+    most = g.job[i].k > most ? g.job[i].k : most;
+    rows += g.job[i].m;
+  }
+  if (most <= 64 * V * 8 && rows >= 2048)
+    return most <= 64 * V * 2 ? launch_quantize_kernel<TYPE, 1, 2>(g, st) : launch_quantize_kernel<TYPE, 1, 8>(g, st);
+  return most <= 256 * V * 2 ? launch_quantize_kernel<TYPE, 4, 2>(g, st) : launch_quantize_kernel<TYPE, 4, 8>(g, st);
+}
+
+hipError_t launch_i8_quantize(const I8QuantizeArgs& g, hipStream_t st) {
+  for (int type = kI8F32; type <= kI8BF16; ++type) {  // a launch for each type
+    I8QuantizeArgs of{};
+    for (int i = 0; i < g.count; ++i)
+      if (g.job[i].type == type) of.job[of.count++] = g.job[i];
+    if (of.count == 0) continue;
+    const hipError_t err = type == kI8F32 ? launch_quantize_type<kI8F32>(of, st)
+                           : type == kI8F16 ? launch_quantize_type<kI8F16>(of, st) : launch_quantize_type<kI8BF16>(of, st);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 // ----------------------------------------------------------------- products

@@ -826,10 +826,12 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
   if (count < 1 || count > qmm::kI8MaxProblems)
     return fail(QMM_ERR_INVALID_ARG, "%s: count=%d must be in [1, %d]", fn, count, qmm::kI8MaxProblems);
   double outputs = 0;
+  long rows = 0;
   for (int i = 0; i < count; ++i) {
     const qmm_i8_problem& q = problems[i];
     if (q.m < 0 || q.m > kMaxI8Rows)
       return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: m=%d must be in [0, %d]", fn, i, q.m, kMaxI8Rows);
+    rows += q.m;
     if (int st = check_i8_sizes(fn, q.n, q.k)) return st;
     if (int st = check_i8_types(fn, q.x_type, q.y_type)) return st;
     outputs += (double)q.m * q.n;
@@ -845,6 +847,7 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
     if (!aligned(q.y, i8_width(q.y_type)))
       return fail(QMM_ERR_INVALID_ARG, "%s: problem %d: y is not %zu-byte aligned", fn, i, i8_width(q.y_type));
   }
+  if (rows > kMaxI8Rows) return fail(QMM_ERR_INVALID_ARG, "%s: too many rows", fn);
   if (outputs > kMaxI8Outputs) return fail(QMM_ERR_INVALID_ARG, "%s: too many outputs", fn);
   for (int i = 0; i < count; ++i) {  // the problems run together: no y on what another one reads or writes
     const qmm_i8_problem& p = problems[i];

@@ -238,7 +238,7 @@ struct I8QuantizeArgs {
   I8QuantizeJob job[kI8MaxProblems];
   int32_t count;
 };
-hipError_t launch_i8_quantize(I8QuantizeArgs& g, hipStream_t st);
+hipError_t launch_i8_quantize(const I8QuantizeArgs& g, hipStream_t st);
 
 struct I8Problem {
   const void* x;    // codes, or values that the product rounds itself

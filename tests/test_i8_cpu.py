@@ -40,6 +40,7 @@ def call(problems=None, count=None, ws=A, ws_bytes=1 << 40, **kw):
     (dict(x_type=-1), UNS, "type -1 of x"),
     (dict(y_type=I8), UNS, "type 3 of the output"),
     (dict(m=1 << 23, n=4097), INV, "too many outputs"),
+    (dict(problems=[problem(m=1 << 23, n=1), problem(m=1 << 23, n=1, y=Y + (1 << 30))]), INV, "too many rows"),
     (dict(w=None), INV, "null pointer"),
     (dict(w_scales=None), INV, "null pointer"),
     (dict(x=None), INV, "null pointer"),
