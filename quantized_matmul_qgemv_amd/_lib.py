@@ -83,8 +83,8 @@ SIGNATURES = {
     "qmm_lora_workspace_size": (SZ, [C.POINTER(LoraProblem), I, I, I]),
     "qmm_lora": (I, [C.POINTER(LoraProblem), I, P, P, P, I, I, I, I, P, SZ, P]),
     "qmm_i8_quantize": (I, [P, I, P, P, I, I, P]),
-    "qmm_i8_gemm_workspace_size": (SZ, [C.POINTER(I8Problem), I]),
-    "qmm_i8_gemm": (I, [C.POINTER(I8Problem), I, P, SZ, P]),
+    "qmm_i8_gemm_workspace_size": (SZ, [P, I]),  # problems: I8Problem's layout
+    "qmm_i8_gemm": (I, [P, I, P, SZ, P]),
     "qmm_i8_grouped_workspace_size": (SZ, [I, I, I]),
     "qmm_i8_gemm_grouped": (I, [P, P, P, P, I, I, P, SZ, P, I, I, I, I, I, I, P, SZ, P]),
     "qmm_i8_moe_gate_up_swiglu": (I, [P, P, P, P, P, P, I, P, SZ, P, I, I, I, I, I, I, P, SZ, P]),

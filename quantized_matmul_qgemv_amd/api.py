@@ -11,12 +11,13 @@ Tensor conventions (device tensors, contiguous):
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from dataclasses import dataclass
 
 import torch
 
 from . import _lib
-from ._lib import GemmProblem, GemvProblem, I8Problem, LoraProblem, check, lib
+from ._lib import GemmProblem, GemvProblem, LoraProblem, check, lib
 
 GROUP = 64
 
@@ -490,6 +491,7 @@ def lora(x, a, b, adapter_ids, scales=None, base=None, y=None, expert_ids=None,
 
 _TYPES = {torch.float32: _lib.QMM_F32, torch.float16: _lib.QMM_F16, torch.bfloat16: _lib.QMM_BF16,
           torch.int8: _lib.QMM_I8}
+_I8_PROBLEM = struct.Struct("@6P5i4x").pack  # a qmm_i8_problem (a third of the time of its ctypes structure)
 _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 _ROWS = _FLOATS + (torch.int8,)
 _C = (torch.int8,)
@@ -521,13 +523,12 @@ def i8_quantize(x, codes=None, scales=None, stream=None):
 def i8_gemm_workspace(problems, stream=None):
     """A workspace for i8_gemm and i8_gemm_batched calls of these problems (kept
     by the caller; calls that share one must not overlap in time)."""
-    arr = (I8Problem * len(problems))()
+    image = b""
     for i, (w, _, x, _, _, _) in enumerate(problems):
         if x.dtype not in _TYPES:
             raise TypeError(f"problem {i}: x has dtype {x.dtype}, expected one of {_ROWS}")
-        arr[i] = I8Problem(None, None, x.data_ptr(), None, None, None, x.shape[0], w.shape[0], x.shape[1],
-                           _TYPES[x.dtype], 0)
-    need = lib().qmm_i8_gemm_workspace_size(arr, len(problems))
+        image += _I8_PROBLEM(0, 0, x.data_ptr(), 0, 0, 0, x.shape[0], w.shape[0], x.shape[1], _TYPES[x.dtype], 0)
+    need = lib().qmm_i8_gemm_workspace_size(image, len(problems))
     return _empty(max(need, 16), torch.uint8, problems[0][2].device, stream)
 
 
@@ -540,11 +541,15 @@ def i8_gemm_batched(problems, dtype=torch.float32, workspace=None, stream=None):
     None; y fp32, fp16 or bf16, or None for one of `dtype`.  Returns the list of y."""
     if not problems:
         raise ValueError("no problems")
-    d, checked, out = None, [], []
+    d, last, packed, out = None, None, [], []
     for i, (w, ws, x, xs, bias, y) in enumerate(problems):
-        if x.dim() != 2 or w.dim() != 2 or w.shape[1] != x.shape[1]:
+        if x is not last:  # q, k and v share theirs
+            if x.dim() != 2:
+                raise ValueError(f"problem {i}: x must be [m, k], not {tuple(x.shape)}")
+            m, k = x.shape
+            px, last = None, x
+        if w.dim() != 2 or w.shape[1] != k:
             raise ValueError(f"problem {i}: w {tuple(w.shape)} and x {tuple(x.shape)} must be [n, k] and [m, k]")
-        m, k = x.shape
         n = w.shape[0]
         if ws.shape != (n,):
             raise ValueError(f"problem {i}: w_scales must be [{n}], not {tuple(ws.shape)}")
@@ -556,17 +561,19 @@ def i8_gemm_batched(problems, dtype=torch.float32, workspace=None, stream=None):
             y = _empty((m, n), dtype, x.device, stream)
         elif y.shape != (m, n):
             raise ValueError(f"problem {i}: y must be [{m}, {n}], not {tuple(y.shape)}")
-        if d is None:
-            d = _device_of(x, "x")
-        checked.append(I8Problem(_ptr(w, "w", _C, d), _ptr(ws, "w_scales", _Y, d), _ptr(x, "x", _ROWS, d),
-                                 _ptr(xs, "x_scales", _Y, d), _ptr(bias, "bias", _Y, d), _ptr(y, "y", _FLOATS, d),
-                                 m, n, k, _TYPES[x.dtype], _TYPES[y.dtype]))
+        if px is None:
+            if d is None:
+                d = _device_of(x, "x")
+            px, x_type = _ptr(x, "x", _ROWS, d), _TYPES[x.dtype]
+        packed.append(_I8_PROBLEM(_ptr(w, "w", _C, d), _ptr(ws, "w_scales", _Y, d), px, _ptr(xs, "x_scales", _Y, d) or 0,
+                                  _ptr(bias, "bias", _Y, d) or 0, _ptr(y, "y", _FLOATS, d), m, n, k, x_type,
+                                  _TYPES[y.dtype]))
         out.append(y)
-    arr = (I8Problem * len(checked))(*checked)
+    image = packed[0] if len(packed) == 1 else b"".join(packed)
     if workspace is None:
-        need = lib().qmm_i8_gemm_workspace_size(arr, len(checked))
+        need = lib().qmm_i8_gemm_workspace_size(image, len(packed))
         workspace = _empty(need, torch.uint8, out[0].device, stream) if need else None
-    check(lib().qmm_i8_gemm(arr, len(checked), _ptr(workspace, "workspace", (torch.uint8,), d),
+    check(lib().qmm_i8_gemm(image, len(packed), _ptr(workspace, "workspace", (torch.uint8,), d),
                             0 if workspace is None else workspace.numel(), _stream_on(stream, d)))
     return out
 

@@ -218,7 +218,7 @@ W, WS, XF = z(8, 64, dtype=torch.int8), z(8), z(3, 64, dtype=torch.float16)
 @pytest.mark.parametrize("error, text, f", [
     (ValueError, "no problems", lambda: qmm.i8_gemm_batched([])),
     (ValueError, "must be \\[n, k\\]", lambda: qmm.i8_gemm(W, WS, z(3, 32, dtype=torch.float16))),
-    (ValueError, "must be \\[n, k\\]", lambda: qmm.i8_gemm(W, WS, z(64, dtype=torch.float16))),
+    (ValueError, "x must be \\[m, k\\]", lambda: qmm.i8_gemm(W, WS, z(64, dtype=torch.float16))),
     (ValueError, "w_scales must be \\[8\\]", lambda: qmm.i8_gemm(W, z(7), XF)),
     (ValueError, "x_scales must be \\[3\\]", lambda: qmm.i8_gemm(W, WS, XF, z(4))),
     (ValueError, "bias must be \\[8\\]", lambda: qmm.i8_gemm(W, WS, XF, bias=z(1))),
