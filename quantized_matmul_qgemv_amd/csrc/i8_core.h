@@ -98,9 +98,11 @@ __device__ __forceinline__ int i8_key(int r) {
 // GATED: of each 32 of the tile's BN rows of W 16 are at `wbase` (gate) and the
 // same 16 at `wbase2` (up), so that both products of an output stand in one
 // lane, eight registers apart.
-template <class S, bool GATED, class XRow, class WRow>
+// `behind` is called behind the first copies.
+template <class S, bool GATED, class XRow, class WRow, class Behind>
 __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const int8_t* wbase, const int8_t* wbase2,
-                                        WRow w_row, int k, int s0, int s1, char* lds, i32x16 (&acc)[S::TM][S::TN]) {
+                                        WRow w_row, int k, int s0, int s1, char* lds, i32x16 (&acc)[S::TM][S::TN],
+                                        Behind behind) {
   // 16 rows are 2 copies (of 8 rows) or one: which base a copy has is its wave's alone
   static_assert(!GATED || (S::RC == 8 && S::WAVES % 4 == 0), "a wave's copies are all gate's or all up's");
   const int lane = threadIdx.x & 63;
@@ -175,6 +177,7 @@ __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const i
 #pragma unroll
   for (int s = 0; s < S::ST; ++s)
     if (s0 + s < s1) copy(s0 + s, s);
+  behind();
   if (s0 + S::ST <= s1) join(std::integral_constant<int, S::ST - 1>{});
   else join(None{});
   read(0, 0, a[0], b[0]);
@@ -341,15 +344,19 @@ __device__ __forceinline__ void i8_finish(const i32x16 (&acc)[S::TM][S::TN], con
           }
         }
       } else {
-        const int columns = 128 / width;
-#pragma unroll 1
-        for (int t = lane; t < 32 * columns; t += 64) {
-          const int rr = t / columns, c = t % columns;
-          if (r0 + rr >= rows || c >= have) continue;
-          const size_t at = (size_t)ys[r0 + rr] * n + n0 + s0 + c;
-          const char* from = out + rr * kI8OutRow + c * width;
-          if (width == 4) static_cast<uint32_t*>(y)[at] = *reinterpret_cast<const uint32_t*>(from);
-          else static_cast<uint16_t*>(y)[at] = *reinterpret_cast<const uint16_t*>(from);
+        // number by number, a whole row (two of 4 bytes) of the 128 bytes at a time
+        const int two = width == 4;
+        const int c = two ? r : lane, step = 1 + two;
+        const bool in = c < have;
+        const char* from = out + (two ? h : 0) * kI8OutRow + c * width;
+        const size_t first = (size_t)n0 + s0 + c;
+#pragma unroll 4
+        for (int t = 0; t < 32; t += step) {
+          const int rr = r0 + t + (two ? h : 0);
+          if (!in || rr >= rows) continue;
+          const size_t at = (size_t)ys[rr] * n + first;
+          if (two) static_cast<uint32_t*>(y)[at] = *reinterpret_cast<const uint32_t*>(from + t * kI8OutRow);
+          else static_cast<uint16_t*>(y)[at] = *reinterpret_cast<const uint16_t*>(from + t * kI8OutRow);
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

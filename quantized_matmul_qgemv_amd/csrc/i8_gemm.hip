@@ -130,13 +130,15 @@ __global__ __launch_bounds__(S::THREADS) void i8_gemm_kernel(I8GemmArgs g, int s
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) acc[i][j] = i32x16{};
   I8Scales<S> scales;
-  scales.load([&](int i) { return m0 + (i < rows ? i : rows - 1); }, [&](int, int row) { return p.sx[row]; },
-              [&](int i) { return p.sw[n0 + (i < cols ? i : cols - 1)]; },
-              [&](int i) { return p.bias ? p.bias[n0 + (i < cols ? i : cols - 1)] : 0.0f; });
+  auto load = [&]() {
+    scales.load([&](int i) { return m0 + (i < rows ? i : rows - 1); }, [&](int, int row) { return p.sx[row]; },
+                [&](int i) { return p.sw[n0 + (i < cols ? i : cols - 1)]; },
+                [&](int i) { return p.bias ? p.bias[n0 + (i < cols ? i : cols - 1)] : 0.0f; });
+  };
   const int steps = (p.k + S::BK - 1) / S::BK;
   const int s0 = PARTS ? (int)((long)steps * split / splits) : 0, s1 = PARTS ? (int)((long)steps * (split + 1) / splits) : steps;
   i8_tile<S, false>(static_cast<const int8_t*>(p.x) + (size_t)m0 * p.k, [&](int i) { return i < rows ? i : rows - 1; },
-                    p.w + (size_t)n0 * p.k, p.w, [&](int i) { return i < cols ? i : cols - 1; }, p.k, s0, s1, lds, acc);
+                    p.w + (size_t)n0 * p.k, p.w, [&](int i) { return i < cols ? i : cols - 1; }, p.k, s0, s1, lds, acc, load);
   void* y = PARTS ? static_cast<void*>(p.sums + (size_t)split * p.m * p.n) : p.y;
   i8_finish<S, false, PARTS>(acc, scales, lds, y, p.y_type, !PARTS && p.bias != nullptr, p.n, n0, rows, cols);
 }

@@ -32,6 +32,9 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
   moe_tile_of(n_tiles, kMoeRun * g.subs, tile, tn);
   const int sub = tile % g.subs;
   tile /= g.subs;
+  // the header and the tile on one way to memory (the grid may reach past the list)
+  const MoeTile* list = reinterpret_cast<const MoeTile*>(ws + kPlanHeaderInts + pairs);
+  MoeTile mt = list[tile < g.plan_tiles ? tile : 0];  // in scalar registers
   // a plan built for other counts is not used: the whole output becomes NaN
   if (ws[1] != g.plan_rows || ws[2] != pairs || ws[3] != g.e) {
     i8_nan_all(g);
@@ -39,8 +42,6 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
   }
   const int listed = __builtin_amdgcn_readfirstlane(ws[0]);
   if (tile >= listed) return;
-  const MoeTile* list = reinterpret_cast<const MoeTile*>(ws + kPlanHeaderInts + pairs);
-  MoeTile mt = list[tile];  // one tile of the workgroup: in scalar registers
   mt.expert = __builtin_amdgcn_readfirstlane(mt.expert);
   mt.start = __builtin_amdgcn_readfirstlane(mt.start);
   mt.rows = __builtin_amdgcn_readfirstlane(mt.rows);
@@ -84,15 +85,17 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
   auto row = [&](int p) { return g.a_row_per_pair ? p : p / g.top_k; };
   I8Scales<S> scales;
   const size_t column = (size_t)mt.expert * g.n + n0;
-  scales.load(pair, [&](int, int p) { return g.sx[row(p)]; },
-              [&](int i) {
-                const bool up = GATED && i % 32 >= 16;
-                if (GATED) i = i / 32 * 16 + i % 16;
-                return (up ? g.sw2 : g.sw)[column + (i < cols ? i : cols - 1)];
-              },
-              [](int) { return 0.0f; });
+  auto load = [&]() {
+    scales.load(pair, [&](int, int p) { return g.sx[row(p)]; },
+                [&](int i) {
+                  const bool up = GATED && i % 32 >= 16;
+                  if (GATED) i = i / 32 * 16 + i % 16;
+                  return (up ? g.sw2 : g.sw)[column + (i < cols ? i : cols - 1)];
+                },
+                [](int) { return 0.0f; });
+  };
   i8_tile<S, GATED>(static_cast<const int8_t*>(g.x), [&](int i) { return row(pair(i)); }, g.w + at, GATED ? g.w2 + at : g.w + at,
-                    [&](int i) { return i < cols ? i : cols - 1; }, g.k, 0, (g.k + S::BK - 1) / S::BK, lds, acc);
+                    [&](int i) { return i < cols ? i : cols - 1; }, g.k, 0, (g.k + S::BK - 1) / S::BK, lds, acc, load);
   i8_finish<S, GATED, false>(acc, scales, lds, g.y, g.y_type, false, g.n, n0, mt.rows, cols);
 }
 
@@ -101,7 +104,8 @@ static hipError_t launch_moe_shape(I8MoeArgs& g, hipStream_t st) {
   constexpr int BC = GATED ? S::BN / 2 : S::BN;
   const int n_tiles = (g.n + BC - 1) / BC;
   g.subs = (g.plan_rows + S::BM - 1) / S::BM;
-  const int m_tiles = max_row_tiles(g.t * g.top_k, g.e, g.plan_rows) * g.subs;
+  g.plan_tiles = max_row_tiles(g.t * g.top_k, g.e, g.plan_rows);
+  const int m_tiles = g.plan_tiles * g.subs;
   hipLaunchKernelGGL((i8_moe_kernel<S, GATED>), dim3(moe_grid(m_tiles, n_tiles, kMoeRun * g.subs)), dim3(S::THREADS), 0, st, g, n_tiles);
   return hipGetLastError();
 }
