@@ -28,20 +28,24 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
   constexpr int BC = GATED ? S::BN / 2 : S::BN;  // output columns
   const int32_t* ws = g.plan;
   const int pairs = g.t * g.top_k;
-  int tile, tn;
-  moe_tile_of(n_tiles, kMoeRun * g.subs, tile, tn);
-  const int sub = tile % g.subs;
-  tile /= g.subs;
-  // the header and the tile on one way to memory (the grid may reach past the list)
-  const MoeTile* list = reinterpret_cast<const MoeTile*>(ws + kPlanHeaderInts + pairs);
-  MoeTile mt = list[tile < g.plan_tiles ? tile : 0];  // in scalar registers
   // a plan built for other counts is not used: the whole output becomes NaN
-  if (ws[1] != g.plan_rows || ws[2] != pairs || ws[3] != g.e) {
+  const i32x4 head = *reinterpret_cast<const i32x4*>(ws);
+  if (head[1] != g.plan_rows || head[2] != pairs || head[3] != g.e) {
     i8_nan_all(g);
     return;
   }
-  const int listed = __builtin_amdgcn_readfirstlane(ws[0]);
+  // Each XCD (workgroups are dealt to the 8 in turn) takes an equal run of the row tiles
+  // that there are, with all their columns: an expert's tiles stand together.
+  const int listed = __builtin_amdgcn_readfirstlane(head[0]);
+  const int each = (listed * g.subs + kMoeXcds - 1) / kMoeXcds, mine = blockIdx.x / kMoeXcds;
+  if (mine >= each * n_tiles) return;
+  const int tn = mine % n_tiles;
+  int tile = blockIdx.x % kMoeXcds * each + mine / n_tiles;
+  const int sub = tile % g.subs;
+  tile /= g.subs;
   if (tile >= listed) return;
+  const MoeTile* list = reinterpret_cast<const MoeTile*>(ws + kPlanHeaderInts + pairs);
+  MoeTile mt = list[tile];  // in scalar registers
   mt.expert = __builtin_amdgcn_readfirstlane(mt.expert);
   mt.start = __builtin_amdgcn_readfirstlane(mt.start);
   mt.rows = __builtin_amdgcn_readfirstlane(mt.rows);
@@ -104,9 +108,8 @@ static hipError_t launch_moe_shape(I8MoeArgs& g, hipStream_t st) {
   constexpr int BC = GATED ? S::BN / 2 : S::BN;
   const int n_tiles = (g.n + BC - 1) / BC;
   g.subs = (g.plan_rows + S::BM - 1) / S::BM;
-  g.plan_tiles = max_row_tiles(g.t * g.top_k, g.e, g.plan_rows);
-  const int m_tiles = g.plan_tiles * g.subs;
-  hipLaunchKernelGGL((i8_moe_kernel<S, GATED>), dim3(moe_grid(m_tiles, n_tiles, kMoeRun * g.subs)), dim3(S::THREADS), 0, st, g, n_tiles);
+  const int m_tiles = max_row_tiles(g.t * g.top_k, g.e, g.plan_rows) * g.subs;
+  hipLaunchKernelGGL((i8_moe_kernel<S, GATED>), dim3((unsigned)((m_tiles + kMoeXcds - 1) / kMoeXcds) * kMoeXcds * n_tiles), dim3(S::THREADS), 0, st, g, n_tiles);
   return hipGetLastError();
 }
 
@@ -186,14 +189,16 @@ I8Way i8_moe_way(const I8MoeArgs& g) {
 }
 
 // Tile shapes, us a call (plan rows 32: 64 tokens, way back; 64: 2048 tokens, way
-// back; 128: 16384 tokens, gate and up; 128 experts, top-8, 768 x 2048, rounding of
-// the rows included):
-//   plan   64x128   64x256   128x128   128x192   256x192   256x256
-//     32     29.1     26.0      29.8      31.9      42.6      37.8
-//     64    103.0     98.3     104.7      98.2     126.8     115.2
-//    128    625.6    576.6     547.7     499.5     574.9     609.1
-// Two workgroups a CU (80 KB of LDS each) beat larger tiles: one stores while the
-// other multiplies.
+// back; 128: 16384 tokens, gate and up; 128 experts, top-8, 768 x 2048, some experts
+// liked more than others, rounding of the rows included; * with a third stage in LDS):
+//   plan   64x128   64x128*   64x256   64x256*   128x128   128x192   128x256*   256x192
+//     32     26.4      25.7     23.5      26.4      27.0      29.0       27.7      41.1
+//     64     94.0     103.4       95     105.2      97.5      93.1      100.4     117.5
+//    128    616.9     690.8      583     704.9      558.6     505.4      594.8     582.1
+// Two workgroups a CU (80 KB of LDS each) beat larger tiles and longer rings: one
+// stores while the other multiplies.  Equal runs of row tiles for the XCDs, by the
+// number that there is, beat runs of eight dealt in turn where tiles are few (333
+// tokens on 35 experts: 25.1 -> 20.7).
 hipError_t launch_i8_moe(I8MoeArgs& g, I8Way way, hipStream_t st) {
   if (way.few) return g.w2 ? launch_moe_few_type<true>(g, st) : launch_moe_few_type<false>(g, st);
   if (way.shape == 1) {

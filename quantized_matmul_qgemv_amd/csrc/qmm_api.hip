@@ -957,7 +957,7 @@ static int i8_routed(const char* fn, const int8_t* w, const float* w_scales, con
   if (overlap(y, y_bytes, x, (size_t)rows * k * i8_width(x_type)))
     return fail(QMM_ERR_INVALID_ARG, "%s: the output overlaps its rows", fn);
   qmm::I8MoeArgs g{x, x_scales, w, w_scales, w2, w2_scales, static_cast<const int32_t*>(plan),
-                   y, t, top_k, e, n, k, per_pair, x_type, y_type, qmm::moe_plan_rows((int)pairs, e), 0, 1};
+                   y, t, top_k, e, n, k, per_pair, x_type, y_type, qmm::moe_plan_rows((int)pairs, e), 1};
   const qmm::I8Way way = qmm::i8_moe_way(g);
   if (x_type != QMM_I8 && !way.staged) {
     qmm::I8QuantizeArgs qa{};

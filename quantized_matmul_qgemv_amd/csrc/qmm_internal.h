@@ -275,7 +275,6 @@ struct I8MoeArgs {
   void* y;
   int32_t t, top_k, e, n, k, a_row_per_pair, x_type, y_type;
   int32_t plan_rows;  // row tile of the plan
-  int32_t plan_tiles; // most row tiles that it can list
   int32_t subs;       // workgroups that share one of its row tiles
 };
 I8Way i8_moe_way(const I8MoeArgs& g);
