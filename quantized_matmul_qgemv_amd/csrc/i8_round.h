@@ -3,8 +3,9 @@
 // s = fp32(max |x| / 127), q = rint(x / s): which whole number is nearest to
 // the exact quotient, ties to even.  n = rint(x * (1 / s)) is that number or its
 // neighbour; the remainder x - n s is a multiple of half a unit in the last
-// place of s and not much larger than s / 2, so one fma gives it exactly and it
-// decides: below s / 2 n is the nearest.  A row whose largest magnitude is below 2^-119 (where s would
+// place of s (of fp32's smallest number, if that is more) and not much larger than
+// s / 2, so one fma gives it exactly and it decides: n is the nearest if twice the
+// remainder is below s (half of the smallest s would not be exact).  A row whose largest magnitude is below 2^-119 (where s would
 // leave fp32's normal range) has s = 0 and codes 0; one with a NaN or infinity
 // has s = NaN and codes 0.
 #pragma once
@@ -60,11 +61,10 @@ __device__ __forceinline__ float i8_scale(uint32_t top) {
 
 __device__ __forceinline__ int i8_round(float x, float s, float inv) {
   const float n = rintf(x * inv);
-  const float d = fmaf(-n, s, x);
-  const float h = 0.5f * s;
+  const float d = 2.0f * fmaf(-n, s, x);
   const int i = (int)n;
-  const int up = d > h || (d == h && (i & 1));
-  const int down = d < -h || (d == -h && (i & 1));
+  const int up = d > s || (d == s && (i & 1));
+  const int down = d < -s || (d == -s && (i & 1));
   return i + up - down;
 }
 
@@ -88,7 +88,7 @@ __device__ __forceinline__ void i8_codes(const I8Raw<TYPE>& raw, float s, float 
     }
     q[w] = __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u) | __builtin_amdgcn_perm(t[3], t[2], 0x04000C0Cu);
   }
-  if (worst < 0.5f * s) return;
+  if (2.0f * worst < s) return;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     q[w] = 0;

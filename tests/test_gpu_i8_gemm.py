@@ -95,6 +95,26 @@ def test_rows_of_zeros_tiny_huge_and_not_finite(dtype, k):
     assert np.array_equal(codes.cpu().numpy(), q)
 
 
+@pytest.mark.parametrize("k", [16, 2560])
+def test_codes_beside_halves_of_the_smallest_scales(k):
+    """Scales in [2^-126, 2^-125) that are an odd multiple of the smallest number, whose
+    half is not a number of fp32: the numbers to both sides of 1/2 and 3/2 of it."""
+    r = np.random.default_rng(3)
+    unit = 2.0 ** -149
+    top = np.float32(127.0 * unit * r.integers(8460000, 11100000, 512))
+    s = np.float32(top / np.float32(127)).astype(np.float64) / unit
+    j = np.floor(s / 2)
+    near = [sign * (i * s + a) * unit for i in (0, 1) for a in (j, j + 1) for sign in (1, -1)]
+    rows = np.stack(near + [top.astype(np.float64)] * (k - len(near)), axis=1)
+    x = torch.from_numpy(rows.astype(np.float32))
+    assert np.array_equal(f64(x), rows)
+    say("i8 quantize smallest scales", k)
+    codes, scales = qmm.i8_quantize(x.cuda())
+    q, want = ref.rows_f64(rows)
+    assert np.array_equal(scales.cpu().numpy(), want)
+    assert np.array_equal(codes.cpu().numpy(), q)
+
+
 def test_stacked_rows_and_no_rows():
     r = np.random.default_rng(4)
     x = torch.from_numpy(r.standard_normal((3, 5, 64)).astype(np.float32)).cuda()
