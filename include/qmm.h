@@ -470,7 +470,8 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
  *       x's row p / top_k with w_gate and w_up [E, n, k] of the pair's expert
  *       (fp32 until h, of h_type, is rounded)
  *   a, x  of a_type / x_type; with QMM_I8 its scales, one for each row, NULL
- *         otherwise.  rows * k must be below 2^32.
+ *         otherwise.  rows * k must be below 2^32, and the tiles of a call (64 rows
+ *         of an expert by 128 columns or more each) about 2^23 at most.
  * Workspace: qmm_i8_grouped_workspace_size bytes for the rows of a or x (0 with
  * QMM_I8: then it may be NULL), as above. */
 size_t qmm_i8_grouped_workspace_size(int rows, int k, int x_type);

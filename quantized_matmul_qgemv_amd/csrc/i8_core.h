@@ -44,7 +44,7 @@ __device__ __forceinline__ void i8_copy(uint32_t lds, i32x4 base, uint32_t voff,
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(base), "s"(soff)
-               : "memory");
+               : "memory", "m0");
 }
 
 // All but this wave's last N copies have landed.

@@ -102,7 +102,7 @@ __device__ __forceinline__ void i8_few(const I8FewTile& t, char* lds, XRow x_row
   }
   const int row = li < t.rows ? li : t.rows - 1;
   // codes of x are read along their rows and turned into operands by way of LDS
-  // (44 bytes a clock and CU from L2; in the operands' order 15)
+  // (16 rows, 9728 x 2560, rounding included: 16.4 us; straight into the operands 18.6)
   constexpr int XS = U * 64 + 16;  // bytes of a row of a batch
   char* held = body + wave * 16 * XS;
   uint32_t xo[STAGED ? 1 : U];

@@ -103,13 +103,20 @@ __global__ __launch_bounds__(S::THREADS) void i8_moe_kernel(I8MoeArgs g, int n_t
   i8_finish<S, GATED, false>(acc, scales, lds, g.y, g.y_type, false, g.n, n0, mt.rows, cols);
 }
 
+// Workgroups of a call: whole rounds of the XCDs for as many row tiles as there can be.
+template <class S, bool GATED>
+static long i8_moe_groups(const I8MoeArgs& g) {
+  constexpr int BC = GATED ? S::BN / 2 : S::BN;
+  const long m_tiles = (long)max_row_tiles(g.t * g.top_k, g.e, g.plan_rows) * ((g.plan_rows + S::BM - 1) / S::BM);
+  return (m_tiles + kMoeXcds - 1) / kMoeXcds * kMoeXcds * ((g.n + BC - 1) / BC);
+}
+
 template <class S, bool GATED>
 static hipError_t launch_moe_shape(I8MoeArgs& g, hipStream_t st) {
   constexpr int BC = GATED ? S::BN / 2 : S::BN;
   const int n_tiles = (g.n + BC - 1) / BC;
   g.subs = (g.plan_rows + S::BM - 1) / S::BM;
-  const int m_tiles = max_row_tiles(g.t * g.top_k, g.e, g.plan_rows) * g.subs;
-  hipLaunchKernelGGL((i8_moe_kernel<S, GATED>), dim3((unsigned)((m_tiles + kMoeXcds - 1) / kMoeXcds) * kMoeXcds * n_tiles), dim3(S::THREADS), 0, st, g, n_tiles);
+  hipLaunchKernelGGL((i8_moe_kernel<S, GATED>), dim3((unsigned)i8_moe_groups<S, GATED>(g)), dim3(S::THREADS), 0, st, g, n_tiles);
   return hipGetLastError();
 }
 
@@ -188,6 +195,18 @@ I8Way i8_moe_way(const I8MoeArgs& g) {
   return way;
 }
 
+using I8MoeTall = I8Shape<128, 192, 4, 2, 2, 128>;
+using I8MoeFlat = I8Shape<64, 256, 2, 4, 2, 128>;
+
+// Few rows: at most 16 row tiles of 2^21 columns, always below.
+bool i8_moe_fits(const I8MoeArgs& g, I8Way way) {
+  if (way.few) return true;
+  long threads;
+  if (way.shape == 1) threads = (g.w2 ? i8_moe_groups<I8MoeTall, true>(g) : i8_moe_groups<I8MoeTall, false>(g)) * I8MoeTall::THREADS;
+  else threads = (g.w2 ? i8_moe_groups<I8MoeFlat, true>(g) : i8_moe_groups<I8MoeFlat, false>(g)) * I8MoeFlat::THREADS;
+  return threads < 1l << 32;
+}
+
 // Tile shapes, us a call (plan rows 32: 64 tokens, way back; 64: 2048 tokens, way
 // back; 128: 16384 tokens, gate and up; 128 experts, top-8, 768 x 2048, some experts
 // liked more than others, rounding of the rows included; * with a third stage in LDS):
@@ -201,12 +220,8 @@ I8Way i8_moe_way(const I8MoeArgs& g) {
 // tokens on 35 experts: 25.1 -> 20.7).
 hipError_t launch_i8_moe(I8MoeArgs& g, I8Way way, hipStream_t st) {
   if (way.few) return g.w2 ? launch_moe_few_type<true>(g, st) : launch_moe_few_type<false>(g, st);
-  if (way.shape == 1) {
-    using S = I8Shape<128, 192, 4, 2, 2, 128>;
-    return g.w2 ? launch_moe_shape<S, true>(g, st) : launch_moe_shape<S, false>(g, st);
-  }
-  using S = I8Shape<64, 256, 2, 4, 2, 128>;
-  return g.w2 ? launch_moe_shape<S, true>(g, st) : launch_moe_shape<S, false>(g, st);
+  if (way.shape == 1) return g.w2 ? launch_moe_shape<I8MoeTall, true>(g, st) : launch_moe_shape<I8MoeTall, false>(g, st);
+  return g.w2 ? launch_moe_shape<I8MoeFlat, true>(g, st) : launch_moe_shape<I8MoeFlat, false>(g, st);
 }
 
 }  // namespace qmm

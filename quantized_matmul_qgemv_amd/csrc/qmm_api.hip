@@ -959,6 +959,8 @@ static int i8_routed(const char* fn, const int8_t* w, const float* w_scales, con
   qmm::I8MoeArgs g{x, x_scales, w, w_scales, w2, w2_scales, static_cast<const int32_t*>(plan),
                    y, t, top_k, e, n, k, per_pair, x_type, y_type, qmm::moe_plan_rows((int)pairs, e), 1};
   const qmm::I8Way way = qmm::i8_moe_way(g);
+  if (!qmm::i8_moe_fits(g, way))
+    return fail(QMM_ERR_INVALID_ARG, "%s: t=%d top_k=%d e=%d n=%d: too many tiles", fn, t, top_k, e, n);
   if (x_type != QMM_I8 && !way.staged) {
     qmm::I8QuantizeArgs qa{};
     int8_t* codes = static_cast<int8_t*>(workspace);

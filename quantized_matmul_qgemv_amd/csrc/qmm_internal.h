@@ -278,6 +278,7 @@ struct I8MoeArgs {
   int32_t subs;       // workgroups that share one of its row tiles
 };
 I8Way i8_moe_way(const I8MoeArgs& g);
+bool i8_moe_fits(const I8MoeArgs& g, I8Way way);  // its grid: below 2^32 threads
 hipError_t launch_i8_moe(I8MoeArgs& g, I8Way way, hipStream_t st);
 
 hipError_t launch_quantize(const float* w, uint32_t* words, uint16_t* s, uint16_t* b, int n,

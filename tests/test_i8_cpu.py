@@ -197,6 +197,13 @@ def test_routed_refusals(gated, kw, status, text):
     assert text in _lib.last_error(), _lib.last_error()
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_refusal_of_a_grid_past_32_bits(gated):
+    """1024 experts by 2^21 columns: at least 2048 row tiles by 8192 column tiles."""
+    assert routed(gated, t=8192, top_k=2, e=1024, n=1 << 21, k=16, y=1 << 45, plan_bytes=1 << 30) == INV
+    assert "too many tiles" in _lib.last_error(), _lib.last_error()
+
+
 def test_refusals_of_one_routed_call_only():
     assert routed(False, per_pair=2) == INV and "a_row_per_pair" in _lib.last_error()
     # with a row for each pair there are twice as many
