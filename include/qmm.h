@@ -463,7 +463,7 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
 /* The experts' products of a routed layer, from a plan of qmm_moe_route for the
  * same (t, top_k, e): pairs, rows and out-of-range experts (NaN rows) as in
  * qmm_qgemm_grouped_routed; a plan built for other counts makes the whole
- * output NaN.
+ * output NaN.  The output must not overlap any operand, nor the plan.
  *   qmm_i8_gemm_grouped  y[p, :] = the product of row(p) of a with w [E, n, k] of
  *       the pair's expert, w_scales [E, n]; y [t * top_k, n] of y_type
  *   qmm_i8_moe_gate_up_swiglu  h[p, :] = silu(g) u with g and u the products of

@@ -953,9 +953,22 @@ static int i8_routed(const char* fn, const int8_t* w, const float* w_scales, con
       return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
     CHECK_PTR(workspace, 16);
   }
-  const size_t y_bytes = (size_t)pairs * n * i8_width(y_type);
-  if (overlap(y, y_bytes, x, (size_t)rows * k * i8_width(x_type)))
-    return fail(QMM_ERR_INVALID_ARG, "%s: the output overlaps its rows", fn);
+  // every operand is read while other workgroups write the output
+  const size_t y_bytes = (size_t)pairs * n * i8_width(y_type), columns = (size_t)e * n;
+  const struct {
+    const void* p;
+    size_t bytes;
+    const char* what;
+  } operands[] = {{x, (size_t)rows * k * i8_width(x_type), "its rows"},
+                  {x_scales, (size_t)rows * 4, "its rows' scales"},
+                  {w, columns * k, "the weights"},
+                  {w2, columns * k, "the weights"},
+                  {w_scales, columns * 4, "the weights' scales"},
+                  {w2_scales, columns * 4, "the weights' scales"},
+                  {plan, qmm::grouped_workspace_bytes(t, top_k, e, 0), "the plan"}};
+  for (const auto& o : operands)
+    if (o.p != nullptr && overlap(y, y_bytes, o.p, o.bytes))
+      return fail(QMM_ERR_INVALID_ARG, "%s: the output overlaps %s", fn, o.what);
   qmm::I8MoeArgs g{x, x_scales, w, w_scales, w2, w2_scales, static_cast<const int32_t*>(plan),
                    y, t, top_k, e, n, k, per_pair, x_type, y_type, qmm::moe_plan_rows((int)pairs, e), 1};
   const qmm::I8Way way = qmm::i8_moe_way(g);

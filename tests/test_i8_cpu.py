@@ -262,3 +262,43 @@ def test_python_routed_refusals(error, text, kw):
     with pytest.raises(error, match=text):
         qmm.i8_moe_gate_up_swiglu((f["w"], f["ws"]), (f["w"], f["ws"]), f["a"], f["expert_ids"], plan, x_scales=f["sa"],
                                   h=f["y"])
+
+
+# ------------------------------------------- outputs and workspaces on what a call reads
+
+OUT = M * 2 * N * 4  # bytes of a routed call's output
+W_BYTES = 4 * N * K
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kw, text", [
+    (dict(w=Y), "the weights"),
+    (dict(w=Y - W_BYTES + 16), "the weights"),
+    (dict(ws=Y + OUT - 4), "the weights' scales"),
+    (dict(ws=Y - 4 * N * 4 + 4), "the weights' scales"),
+    (dict(a_type=I8, sa=Y + 4), "its rows' scales"),
+    (dict(plan=Y), "the plan"),
+    (dict(plan=Y + OUT - 16), "the plan"),
+])
+def test_routed_outputs_on_operands(gated, kw, text):
+    assert routed(gated, **kw) == INV, _lib.last_error()
+    assert _lib.last_error().endswith("the output overlaps " + text), _lib.last_error()
+
+
+@pytest.mark.parametrize("kw, text", [(dict(w2=Y + OUT - 16), "the weights"), (dict(ws2=Y), "the weights' scales")])
+def test_routed_outputs_on_the_second_weights(kw, text):
+    assert routed(True, **kw) == INV, _lib.last_error()
+    assert _lib.last_error().endswith("the output overlaps " + text), _lib.last_error()
+
+
+BIG, BIG_OUT, BIG_W, BIG_S = 1 << 45, 16384 * (1 << 21) * 4, 1024 * (1 << 21) * 16, 1024 * (1 << 21) * 4
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kw", [dict(w=BIG - BIG_W), dict(w=BIG + BIG_OUT), dict(ws=BIG + BIG_OUT), dict(ws=BIG - BIG_S),
+                                dict(plan=BIG + BIG_OUT), dict(w2=BIG + BIG_OUT, ws2=BIG - BIG_S),
+                                dict(a_type=I8, sa=BIG + BIG_OUT), dict(a_type=I8, sa=BIG - 8192 * 4)])
+def test_routed_outputs_beside_operands(gated, kw):
+    """Taken as far as the number of tiles, which is refused behind every overlap of the output."""
+    assert routed(gated, t=8192, top_k=2, e=1024, n=1 << 21, k=16, y=BIG, plan_bytes=1 << 30, **kw) == INV
+    assert "too many tiles" in _lib.last_error(), _lib.last_error()
