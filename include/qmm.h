@@ -439,8 +439,9 @@ int qmm_i8_quantize(const void* x, int x_type, int8_t* codes, float* scales, int
  *   bias      [n] fp32 or NULL
  * Workspace: qmm_i8_gemm_workspace_size bytes (x, m, n, k and x_type of the
  * problems are read; 0 for sizes that are refused, and where none is needed:
- * then it may be NULL), contents on entry do not matter; calls (and captured
- * graphs) that share one must not run concurrently.  m = 0: the problem does
+ * then it may be NULL), contents on entry do not matter; it must not overlap an
+ * operand or an output; calls (and captured graphs) that share one must not run
+ * concurrently.  m = 0: the problem does
  * nothing.  One to three launches, by sizes (one more for each further type of x). */
 typedef struct {
   const int8_t* w;

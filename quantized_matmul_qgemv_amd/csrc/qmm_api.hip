@@ -881,6 +881,18 @@ int qmm_i8_gemm(const qmm_i8_problem* problems, int count, void* workspace, size
     if (workspace == nullptr || workspace_bytes < need)
       return fail(QMM_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace ? workspace_bytes : 0, need);
     CHECK_PTR(workspace, 16);
+    for (int i = 0; i < count; ++i) {  // codes and sums are written there before the products read
+      const qmm_i8_problem& q = problems[i];
+      if (q.m == 0) continue;
+      const char* what = nullptr;
+      if (overlap(workspace, need, q.x, (size_t)q.m * q.k * i8_width(q.x_type))) what = "x";
+      else if (overlap(workspace, need, q.w, (size_t)q.n * q.k)) what = "w";
+      else if (overlap(workspace, need, q.w_scales, (size_t)q.n * 4) ||
+               (q.x_scales && overlap(workspace, need, q.x_scales, (size_t)q.m * 4))) what = "scales";
+      else if (q.bias && overlap(workspace, need, q.bias, (size_t)q.n * 4)) what = "bias";
+      else if (overlap(workspace, need, q.y, (size_t)q.m * q.n * i8_width(q.y_type))) what = "y";
+      if (what) return fail(QMM_ERR_INVALID_ARG, "%s: the workspace overlaps the %s of problem %d", fn, what, i);
+    }
   }
   char* next = static_cast<char*>(workspace);
   if (!way.staged) {
@@ -975,6 +987,10 @@ static int i8_routed(const char* fn, const int8_t* w, const float* w_scales, con
   if (!qmm::i8_moe_fits(g, way))
     return fail(QMM_ERR_INVALID_ARG, "%s: t=%d top_k=%d e=%d n=%d: too many tiles", fn, t, top_k, e, n);
   if (x_type != QMM_I8 && !way.staged) {
+    if (overlap(workspace, need, y, y_bytes)) return fail(QMM_ERR_INVALID_ARG, "%s: the workspace overlaps the output", fn);
+    for (const auto& o : operands)
+      if (o.p != nullptr && overlap(workspace, need, o.p, o.bytes))
+        return fail(QMM_ERR_INVALID_ARG, "%s: the workspace overlaps %s", fn, o.what);
     qmm::I8QuantizeArgs qa{};
     int8_t* codes = static_cast<int8_t*>(workspace);
     float* scales = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)rows * k));

@@ -302,3 +302,60 @@ def test_routed_outputs_beside_operands(gated, kw):
     """Taken as far as the number of tiles, which is refused behind every overlap of the output."""
     assert routed(gated, t=8192, top_k=2, e=1024, n=1 << 21, k=16, y=BIG, plan_bytes=1 << 30, **kw) == INV
     assert "too many tiles" in _lib.last_error(), _lib.last_error()
+
+
+NEED = 1536  # bytes of the workspace of 20 x 64 rows: codes and scales
+SPACE = 0x60000000
+
+
+@pytest.mark.parametrize("kw, text", [
+    (dict(x=SPACE), "x"),
+    (dict(x=SPACE + NEED - 16), "x"),
+    (dict(w=SPACE - N * K + 16), "w"),
+    (dict(w_scales=SPACE + NEED - 4), "scales"),
+    (dict(bias=SPACE), "bias"),
+    (dict(y=SPACE + NEED - 4), "y"),
+    (dict(y=SPACE - ROWS + 4), "y"),
+])
+def test_workspaces_on_operands(kw, text):
+    assert call(ws=SPACE, **kw) == INV, _lib.last_error()
+    assert _lib.last_error().endswith(f"the workspace overlaps the {text} of problem 0"), _lib.last_error()
+
+
+def test_workspaces_on_the_operands_of_other_problems():
+    """A workspace that the sums of parts of k need, on the scales of given codes."""
+    ps = [problem(x_type=I8, x_scales=A, n=1024, k=8192), problem(x_type=I8, x_scales=SPACE + 64, n=1024, k=8192, y=Y + (1 << 24))]
+    assert call(problems=ps, ws=SPACE) == INV, _lib.last_error()
+    assert _lib.last_error().endswith("the workspace overlaps the scales of problem 1"), _lib.last_error()
+    # no rows, nothing read: what such a problem names does not matter
+    ps = [problem(), problem(m=0, x=SPACE, w=SPACE), problem(y=SPACE, m=M)]
+    assert call(problems=ps, ws=SPACE) == INV, _lib.last_error()
+    assert _lib.last_error().endswith("the workspace overlaps the y of problem 2"), _lib.last_error()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kw, text", [
+    (dict(a=SPACE), "its rows"),
+    (dict(w=SPACE), "the weights"),
+    (dict(ws=SPACE + NEED - 4), "the weights' scales"),
+    (dict(plan=SPACE + NEED - 16), "the plan"),
+    (dict(y=SPACE + NEED - 4), "the output"),
+    (dict(y=SPACE - OUT + 4), "the output"),
+])
+def test_routed_workspaces_on_operands(gated, kw, text):
+    assert routed(gated, wsp=SPACE, **kw) == INV, _lib.last_error()
+    assert _lib.last_error().endswith("the workspace overlaps " + text), _lib.last_error()
+
+
+def test_routed_workspaces_on_the_second_weights():
+    for kw, text in ((dict(w2=SPACE), "the weights"), (dict(ws2=SPACE), "the weights' scales")):
+        assert routed(True, wsp=SPACE, **kw) == INV, _lib.last_error()
+        assert _lib.last_error().endswith("the workspace overlaps " + text), _lib.last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(x=SPACE + NEED), dict(x=SPACE - M * K * 2), dict(w=SPACE - N * K), dict(w_scales=SPACE + NEED), dict(bias=SPACE - N * 4)])
+def test_workspaces_beside_operands(kw):
+    """Only the y of the second problem, the last that is looked at, is on the workspace."""
+    ps = [problem(**kw), problem(n=1, x=kw.get("x", X), y=SPACE + 256)]
+    assert call(problems=ps, ws=SPACE) == INV
+    assert _lib.last_error().endswith("the workspace overlaps the y of problem 1"), _lib.last_error()
