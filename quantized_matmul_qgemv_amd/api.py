@@ -497,6 +497,14 @@ _ROWS = _FLOATS + (torch.int8,)
 _C = (torch.int8,)
 
 
+def _int32(**sizes):
+    """The entry points take sizes as 32-bit integers, and ctypes would cut off
+    what is above them."""
+    for name, v in sizes.items():
+        if v >= 1 << 31:
+            raise ValueError(f"{name}={v} must be below 2^31")
+
+
 def i8_quantize(x, codes=None, scales=None, stream=None):
     """(codes int8 [m, k], scales fp32 [m]) of the rows of x [m, k] (fp32, fp16 or
     bf16), via qmm_i8_quantize: scale = max |x| / 127, code = the whole number
@@ -506,6 +514,7 @@ def i8_quantize(x, codes=None, scales=None, stream=None):
     if x.dim() < 2:
         raise ValueError(f"x must be [m, k], not {tuple(x.shape)}")
     k = x.shape[-1]
+    _int32(m=x.shape[:-1].numel(), k=k)
     if codes is None:
         codes = _empty(x.shape, torch.int8, x.device, stream)
     elif codes.shape != x.shape:
@@ -527,6 +536,7 @@ def i8_gemm_workspace(problems, stream=None):
     for i, (w, _, x, _, _, _) in enumerate(problems):
         if x.dtype not in _TYPES:
             raise TypeError(f"problem {i}: x has dtype {x.dtype}, expected one of {_ROWS}")
+        _int32(m=x.shape[0], n=w.shape[0], k=x.shape[1])
         image += _I8_PROBLEM(0, 0, x.data_ptr(), 0, 0, 0, x.shape[0], w.shape[0], x.shape[1], _TYPES[x.dtype], 0)
     need = lib().qmm_i8_gemm_workspace_size(image, len(problems))
     return _empty(max(need, 16), torch.uint8, problems[0][2].device, stream)
@@ -547,10 +557,14 @@ def i8_gemm_batched(problems, dtype=torch.float32, workspace=None, stream=None):
             if x.dim() != 2:
                 raise ValueError(f"problem {i}: x must be [m, k], not {tuple(x.shape)}")
             m, k = x.shape
+            if (m | k) >> 31:  # looked at before the call by names, 0.2 us of a decode step's 8
+                _int32(m=m, k=k)
             px, last = None, x
         if w.dim() != 2 or w.shape[1] != k:
             raise ValueError(f"problem {i}: w {tuple(w.shape)} and x {tuple(x.shape)} must be [n, k] and [m, k]")
         n = w.shape[0]
+        if n >> 31:
+            _int32(n=n)
         if ws.shape != (n,):
             raise ValueError(f"problem {i}: w_scales must be [{n}], not {tuple(ws.shape)}")
         if xs is not None and xs.shape != (m,):
@@ -589,6 +603,7 @@ def i8_grouped_workspace(x, stream=None):
     x's (kept by the caller; calls that share one must not overlap in time)."""
     if x.dtype not in _TYPES:
         raise TypeError(f"x has dtype {x.dtype}, expected one of {_ROWS}")
+    _int32(rows=x.shape[0], k=x.shape[1])
     need = lib().qmm_i8_grouped_workspace_size(x.shape[0], x.shape[1], _TYPES[x.dtype])
     return _empty(max(need, 16), torch.uint8, x.device, stream)
 
@@ -602,6 +617,8 @@ def _i8_routed(weights, x, x_scales, expert_ids, plan, per_pair, y, dtype, works
     if w.dim() != 3 or x.dim() != 2 or w.shape[2] != x.shape[1]:
         raise ValueError(f"w {tuple(w.shape)} and the rows {tuple(x.shape)} must be [E, n, k] and [rows, k]")
     e, n, k = w.shape
+    if (t | top_k | t * top_k | e | n | k) >> 31:
+        _int32(t=t, top_k=top_k, pairs=t * top_k, e=e, n=n, k=k)
     for v, vs in weights:
         if v.shape != (e, n, k) or vs.shape != (e, n):
             raise ValueError(f"weights {tuple(v.shape)} and their scales {tuple(vs.shape)} must be [{e}, {n}, {k}] and [{e}, {n}]")

@@ -359,3 +359,42 @@ def test_workspaces_beside_operands(kw):
     ps = [problem(**kw), problem(n=1, x=kw.get("x", X), y=SPACE + 256)]
     assert call(problems=ps, ws=SPACE) == INV
     assert _lib.last_error().endswith("the workspace overlaps the y of problem 1"), _lib.last_error()
+
+
+# --------------------------------------------------- sizes that 32 bits do not hold
+
+def far(*shape, dtype=torch.int8):
+    """A tensor without memory: only its sizes are looked at."""
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+LONG = (1 << 32) + 16  # 16 in 32 bits
+
+
+@pytest.mark.parametrize("text, f", [
+    ("m=4294967312", lambda: qmm.i8_quantize(far(LONG, 16, dtype=torch.float16))),
+    ("m=4294967312", lambda: qmm.i8_quantize(far((1 << 28) + 1, 16, 16, dtype=torch.float16))),
+    ("k=4294967312", lambda: qmm.i8_quantize(far(1, LONG, dtype=torch.float16))),
+    ("m=4294967312", lambda: qmm.i8_gemm(far(8, 16), far(8, dtype=torch.float32), far(LONG, 16), far(LONG, dtype=torch.float32))),
+    ("n=4294967312", lambda: qmm.i8_gemm(far(LONG, 16), far(LONG, dtype=torch.float32), far(3, 16, dtype=torch.float16))),
+    ("k=4294967312", lambda: qmm.i8_gemm(far(8, LONG), far(8, dtype=torch.float32), far(3, LONG, dtype=torch.float16))),
+    ("m=4294967312", lambda: qmm.i8_gemm_workspace([(far(8, 16), None, far(LONG, 16), None, None, None)])),
+    ("n=4294967312", lambda: qmm.i8_gemm_workspace([(far(LONG, 16), None, far(3, 16), None, None, None)])),
+    ("rows=4294967312", lambda: qmm.i8_grouped_workspace(far(LONG, 16, dtype=torch.float16))),
+    ("k=4294967312", lambda: qmm.i8_grouped_workspace(far(3, LONG, dtype=torch.float16))),
+])
+def test_sizes_past_32_bits(text, f):
+    with pytest.raises(ValueError, match=text + " must be below 2"):
+        f()
+
+
+@pytest.mark.parametrize("text, t, top_k, e, n, k", [
+    ("t=4294967312", LONG, 1, 2, 8, 16), ("top_k=4294967312", 1, LONG, 2, 8, 16), ("pairs=4294967312", LONG // 16, 16, 2, 8, 16),
+    ("e=4294967312", 3, 2, LONG, 8, 16), ("n=4294967312", 3, 2, 2, LONG, 16), ("k=4294967312", 3, 2, 2, 8, LONG)])
+def test_routed_sizes_past_32_bits(text, t, top_k, e, n, k):
+    w, ws = far(e, n, k), far(e, n, dtype=torch.float32)
+    x, ids, plan = far(t, k, dtype=torch.float16), far(t, top_k, dtype=torch.int32), far(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match=text + " must be below 2"):
+        qmm.i8_gemm_grouped(w, ws, x, ids, plan, False)
+    with pytest.raises(ValueError, match=text + " must be below 2"):
+        qmm.i8_moe_gate_up_swiglu((w, ws), (w, ws), x, ids, plan)
