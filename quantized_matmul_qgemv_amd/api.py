@@ -532,8 +532,14 @@ def i8_quantize(x, codes=None, scales=None, stream=None):
 def i8_gemm_workspace(problems, stream=None):
     """A workspace for i8_gemm and i8_gemm_batched calls of these problems (kept
     by the caller; calls that share one must not overlap in time)."""
+    if not problems:
+        raise ValueError("no problems")
     image = b""
     for i, (w, _, x, _, _, _) in enumerate(problems):
+        if x.dim() != 2:
+            raise ValueError(f"problem {i}: x must be [m, k], not {tuple(x.shape)}")
+        if w.dim() != 2 or w.shape[1] != x.shape[1]:
+            raise ValueError(f"problem {i}: w {tuple(w.shape)} and x {tuple(x.shape)} must be [n, k] and [m, k]")
         if x.dtype not in _TYPES:
             raise TypeError(f"problem {i}: x has dtype {x.dtype}, expected one of {_ROWS}")
         _int32(m=x.shape[0], n=w.shape[0], k=x.shape[1])
@@ -603,6 +609,8 @@ def i8_grouped_workspace(x, stream=None):
     x's (kept by the caller; calls that share one must not overlap in time)."""
     if x.dtype not in _TYPES:
         raise TypeError(f"x has dtype {x.dtype}, expected one of {_ROWS}")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, k], not {tuple(x.shape)}")
     _int32(rows=x.shape[0], k=x.shape[1])
     need = lib().qmm_i8_grouped_workspace_size(x.shape[0], x.shape[1], _TYPES[x.dtype])
     return _empty(max(need, 16), torch.uint8, x.device, stream)

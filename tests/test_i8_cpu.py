@@ -398,3 +398,18 @@ def test_routed_sizes_past_32_bits(text, t, top_k, e, n, k):
         qmm.i8_gemm_grouped(w, ws, x, ids, plan, False)
     with pytest.raises(ValueError, match=text + " must be below 2"):
         qmm.i8_moe_gate_up_swiglu((w, ws), (w, ws), x, ids, plan)
+
+
+@pytest.mark.parametrize("text, f", [
+    ("no problems", lambda: qmm.i8_gemm_workspace([])),
+    ("problem 0: x must be \\[m, k\\]", lambda: qmm.i8_gemm_workspace([(W, WS, z(64, dtype=torch.float16), None, None, None)])),
+    ("problem 1: w .* and x .* must be", lambda: qmm.i8_gemm_workspace([(W, WS, XF, None, None, None),
+                                                                     (z(8, 32, dtype=torch.int8), WS, XF, None, None, None)])),
+    ("problem 0: w .* and x .* must be", lambda: qmm.i8_gemm_workspace([(z(8, dtype=torch.int8), WS, XF, None, None, None)])),
+    ("x must be \\[rows, k\\]", lambda: qmm.i8_grouped_workspace(z(64, dtype=torch.float16))),
+    ("x must be \\[rows, k\\]", lambda: qmm.i8_grouped_workspace(z(3, 2, 64, dtype=torch.float16))),
+])
+def test_workspaces_for_operands_of_the_wrong_shape(text, f):
+    """Refused as by the calls that they are for."""
+    with pytest.raises(ValueError, match=text):
+        f()
