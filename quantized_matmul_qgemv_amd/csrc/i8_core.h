@@ -21,6 +21,11 @@
 
 #include "qmm_device.h"
 
+// A result is rounded after each scale and again after the bias, by whichever way
+// it is computed: no product may be drawn into the addition behind it, here and in
+// what includes this.
+#pragma clang fp contract(off)
+
 namespace qmm {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));

@@ -336,3 +336,39 @@ def test_no_rows_and_empty_problems_beside_others():
     assert qmm.i8_gemm(dev(w), dev(ws), x[:0]).shape == (0, 9)
     a, b = qmm.i8_gemm_batched([(dev(w), dev(ws), x[:0], None, None, None), (dev(w), dev(ws), x, None, None, None)])
     assert a.shape == (0, 9) and torch.equal(b, qmm.i8_gemm(dev(w), dev(ws), x))
+
+
+# (m, n, k), QMM_I8_FORCE, QMM_I8_SPLITS: few rows rounded in the product and before it, as codes,
+# tiles with k whole and in parts (widths of 4 and odd ones)
+STEPS = [((1, 1001, 2560), None, None), ((8, 260, 1040), None, None), ((12, 300, 528), None, None),
+         ((64, 332, 1296), "0", "1"), ((64, 333, 1296), "0", "3"), ((64, 332, 1296), "2", "4"), ((300, 517, 400), "5", "1"),
+         ((5, 333, 1296), "1", "1"), ((5, 333, 1296), "1", "2")]
+
+
+@pytest.mark.parametrize("xt", [F16, torch.int8], ids=ids)
+@pytest.mark.parametrize("size,force,splits", STEPS)
+def test_every_way_rounds_after_each_scale_and_after_the_bias(size, force, splits, xt, monkeypatch):
+    """Bit by bit what fp32 arithmetic gives step by step: the bias is about as large as
+    the product, so that a product which is not rounded before the sum shows."""
+    say("i8 gemm steps", size, force, splits, xt)
+    if force is not None:
+        monkeypatch.setenv("QMM_I8_FORCE", force)
+        monkeypatch.setenv("QMM_I8_SPLITS", splits)
+    m, n, k = size
+    r = np.random.default_rng([25, m, n, k])
+    w, ws = weights(r, n, k)
+    if xt == torch.int8:
+        q, s = r.integers(-128, 128, (m, k)).astype(np.int8), (r.random(m) * 0.1).astype(np.float32)
+        x, xs = dev(q), dev(s)
+    else:
+        x, xs = activations(r, m, k, xt), None
+        q, s = ref.rows_f64(f64(x))
+    sums = q.astype(np.float64) @ w.astype(np.float64).T  # whole numbers
+    product = sums.astype(np.float32) * s[:, None] * ws[None, :]
+    b = (product[0] * (r.random(n) - 1.5)).astype(np.float32)
+    want = product + b[None, :]
+    apart = sums.astype(np.float32).astype(np.float64) * s[:, None]
+    fused = (apart.astype(np.float32).astype(np.float64) * ws[None, :] + b[None, :]).astype(np.float32)
+    assert want.dtype == np.float32 and (fused != want).sum() > want.size / 20  # the inputs tell one from the other
+    y = qmm.i8_gemm(dev(w), dev(ws), x, xs, bias=dev(b))
+    assert np.array_equal(y.cpu().numpy(), want)
