@@ -44,13 +44,18 @@ __device__ __forceinline__ i32x4 i8_rows(const void* base) {
 // builtin of the same instruction makes the compiler wait for every copy in
 // flight before any LDS read, which undoes the ring.)  s_nop: a scalar register
 // that a vector instruction has written may be read by a vector memory
-// instruction five wait states later.
+// instruction five wait states later.  The compiler holds m0 for its own and warns of
+// every asm that names it, once for each copy of the code; nothing else in these
+// kernels uses it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void i8_copy(uint32_t lds, i32x4 base, uint32_t voff, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(base), "s"(soff)
                : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // All but this wave's last N copies have landed.
 template <int N>
