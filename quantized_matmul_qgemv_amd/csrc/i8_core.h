@@ -70,11 +70,11 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
-// BM rows of X by BN rows of W on WM x WN waves, a ring of ST stages of BK bytes
-// of k.
-template <int BM_, int BN_, int WM_, int WN_, int ST_, int BK_>
+// BM rows of X by BN rows of W on WM x WN waves, a ring of ST stages of a line
+// (BK bytes) of k.
+template <int BM_, int BN_, int WM_, int WN_, int ST_>
 struct I8Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, BK = BK_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, BK = 128;
   static constexpr int WAVES = WM * WN;
   static constexpr int THREADS = 64 * WAVES;
   static constexpr int TM = BM / WM / 32;  // blocks of 32 x 32 a wave
@@ -83,22 +83,16 @@ struct I8Shape {
   static constexpr int RC = 64 / PIECES;       // rows a copy
   static constexpr int CX = BM / RC;           // copies a step: X's, then W's,
   static constexpr int CW = BN / RC;
-  static constexpr int COPIES = CX + CW;
-  static constexpr int EACH = (COPIES + WAVES - 1) / WAVES;  // dealt to the waves in turn
-  static constexpr int SHORT = COPIES % WAVES;               // waves from here on have one less (0: none)
+  static constexpr int EACH = (CX + CW) / WAVES;  // dealt to the waves in turn
   static constexpr int STAGE = (BM + BN) * BK;
   static constexpr int LDS = ST * STAGE;
-  static_assert(BK == 64 || BK == 128, "half a line or a line");
   static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "whole blocks");
-  static_assert(BM % RC == 0 && BN % (2 * RC) == 0 && WAVES % 2 == 0 && CX % WAVES == 0, "whole copies");
+  static_assert(BM % RC == 0 && BN % RC == 0 && WAVES % 2 == 0 && CX % WAVES == 0 && CW % WAVES == 0, "whole copies");
   static_assert((ST - 1) * EACH <= 63 && ST >= 2, "vmcnt counts to 63");
 };
 
 // Where piece c of row r stands in its row of a stage: XOR with this.
-template <class S>
-__device__ __forceinline__ int i8_key(int r) {
-  return S::BK == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
-}
+__device__ __forceinline__ int i8_key(int r) { return (r >> 1) & 7; }
 
 // One tile.  x_row(i) is the row of x at `xbase` that stands in row i of the
 // tile, w_row(i) likewise (any valid row where the tile reaches past the
@@ -113,8 +107,8 @@ template <class S, bool GATED, class XRow, class WRow, class Behind>
 __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const int8_t* wbase, const int8_t* wbase2,
                                         WRow w_row, int k, int s0, int s1, char* lds, i32x16 (&acc)[S::TM][S::TN],
                                         Behind behind) {
-  // 16 rows are 2 copies (of 8 rows) or one: which base a copy has is its wave's alone
-  static_assert(!GATED || (S::RC == 8 && S::WAVES % 4 == 0), "a wave's copies are all gate's or all up's");
+  // 16 rows are 2 copies: which base a copy has is its wave's alone
+  static_assert(!GATED || S::WAVES % 4 == 0, "a wave's copies are all gate's or all up's");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
@@ -122,7 +116,7 @@ __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const i
   // the copies: RC rows each, of which this lane takes one piece (its key is the
   // same in all: they are an even number of waves apart)
   const int mine = lane / S::PIECES;
-  const int piece = (lane % S::PIECES) ^ i8_key<S>(wave * S::RC + mine);
+  const int piece = (lane % S::PIECES) ^ i8_key(wave * S::RC + mine);
   uint32_t from[S::EACH];
 #pragma unroll
   for (int j = 0; j < S::EACH; ++j) {
@@ -130,7 +124,7 @@ __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const i
     if (j * S::WAVES < S::CX) {
       i = x_row(i);
     } else {
-      i = i - S::BM < S::BN ? i - S::BM : S::BN - 1;
+      i -= S::BM;
       i = w_row(GATED ? i / 32 * 16 + i % 16 : i);
     }
     from[j] = (uint32_t)i * (uint32_t)k + piece * 16;
@@ -141,29 +135,24 @@ __device__ __forceinline__ void i8_tile(const int8_t* xbase, XRow x_row, const i
   const int whole = k / S::BK;            // steps that are whole
   const int pieces = (k % S::BK) / 16;    // pieces of the step behind them
   const uint32_t back = piece >= pieces ? (piece - (pieces - 1)) * 16 : 0;
-  const bool less = S::SHORT != 0 && wave >= S::SHORT;
 
   auto copy = [&](int step, int stage) {
     const uint32_t at = ring + stage * S::STAGE + wave * 1024;
     const uint32_t off = step < whole ? 0 : back;
     const uint32_t soff = (uint32_t)step * S::BK;
 #pragma unroll
-    for (int j = 0; j < S::EACH; ++j) {
-      if (j == S::EACH - 1 && less) break;
-      i8_copy(at + j * S::WAVES * 1024, j * S::WAVES < S::CX ? xr : wr, from[j] - off, soff);
-    }
+    for (int j = 0; j < S::EACH; ++j) i8_copy(at + j * S::WAVES * 1024, j * S::WAVES < S::CX ? xr : wr, from[j] - off, soff);
   };
   // all but the copies of the last N steps have landed, in every wave
   auto join = [&](auto n) {
     constexpr int N = decltype(n)::value;
-    if (less) i8_wait<N * (S::EACH - 1)>();
-    else i8_wait<N * S::EACH>();
+    i8_wait<N * S::EACH>();
     i8_meet();
   };
   using None = std::integral_constant<int, 0>;
 
   const int r = lane & 31, h = lane >> 5;
-  const int key = i8_key<S>(r);
+  const int key = i8_key(r);
   const char* xs = lds + (wm * S::TM * 32 + r) * S::BK;
   const char* ws = lds + (S::BM + wn * S::TN * 32 + r) * S::BK;
   // a step's products of 32 bytes of k; the operands of the next one are read

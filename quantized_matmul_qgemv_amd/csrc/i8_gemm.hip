@@ -356,13 +356,13 @@ hipError_t launch_i8_gemm(I8GemmArgs& g, I8Way way, hipStream_t st) {
     default: return launch_few<kI8Codes>(g, st);
   }
   switch (way.shape) {
-    case 0: return launch_shape<I8Shape<64, 64, 2, 2, 3, 128>>(g, way.splits, st);
-    case 1: return launch_shape<I8Shape<64, 128, 2, 4, 6, 128>>(g, way.splits, st);
-    case 2: return launch_shape<I8Shape<128, 128, 2, 4, 3, 128>>(g, way.splits, st);
-    case 3: return launch_shape<I8Shape<128, 192, 4, 2, 3, 128>>(g, way.splits, st);
-    case 4: return launch_shape<I8Shape<256, 192, 4, 2, 2, 128>>(g, way.splits, st);
-    case 5: return launch_shape<I8Shape<256, 256, 2, 4, 2, 128>>(g, way.splits, st);
-    default: return launch_shape<I8Shape<256, 320, 4, 2, 2, 128>>(g, way.splits, st);
+    case 0: return launch_shape<I8Shape<64, 64, 2, 2, 3>>(g, way.splits, st);
+    case 1: return launch_shape<I8Shape<64, 128, 2, 4, 6>>(g, way.splits, st);
+    case 2: return launch_shape<I8Shape<128, 128, 2, 4, 3>>(g, way.splits, st);
+    case 3: return launch_shape<I8Shape<128, 192, 4, 2, 3>>(g, way.splits, st);
+    case 4: return launch_shape<I8Shape<256, 192, 4, 2, 2>>(g, way.splits, st);
+    case 5: return launch_shape<I8Shape<256, 256, 2, 4, 2>>(g, way.splits, st);
+    default: return launch_shape<I8Shape<256, 320, 4, 2, 2>>(g, way.splits, st);
   }
 }
 

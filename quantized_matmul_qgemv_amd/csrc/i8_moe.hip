@@ -195,8 +195,8 @@ I8Way i8_moe_way(const I8MoeArgs& g) {
   return way;
 }
 
-using I8MoeTall = I8Shape<128, 192, 4, 2, 2, 128>;
-using I8MoeFlat = I8Shape<64, 256, 2, 4, 2, 128>;
+using I8MoeTall = I8Shape<128, 192, 4, 2, 2>;
+using I8MoeFlat = I8Shape<64, 256, 2, 4, 2>;
 
 // Few rows: at most 16 row tiles of 2^21 columns, always below.
 bool i8_moe_fits(const I8MoeArgs& g, I8Way way) {
