@@ -189,3 +189,60 @@ def test_a_routed_layer_end_to_end():
         ww = f64(weights)[:, :, None]
         bound = (5 + top_k) * 1.1 * ref.HALF * (ww * np.abs(pairs)).sum(axis=1)
         assert np.all(np.abs(f64(y) - (ww * pairs).sum(axis=1)) <= bound + 1e-37)
+
+
+@pytest.mark.parametrize("t,top_k,e,n,k,kind", SIZES + [(1, 8, 9, 65, 2064, "any"), (2, 8, 30, 48, 528, "bad"), (16, 1, 3, 70, 96, "one")])
+def test_gate_and_up_of_given_codes(t, top_k, e, n, k, kind):
+    """By the formulas, with codes down to -128, and the bits of the call that rounds x itself."""
+    say("i8 swiglu codes", t, top_k, e, n, k, kind)
+    r = np.random.default_rng([26, t, top_k, e, n, k])
+    gate, up = experts(r, e, n, k), experts(r, e, n, k)
+    G, U = tuple(map(dev, gate)), tuple(map(dev, up))
+    I = some_ids(r, t, top_k, e, kind)
+    D = dev(I)
+    plan = qmm.moe_route(D, e)
+    q, s = r.integers(-128, 128, (t, k)).astype(np.int8), (r.random(t) * 0.02).astype(np.float32)
+    for ht in (F32, F16):
+        h = Guarded((t * top_k, n), ht)
+        qmm.i8_moe_gate_up_swiglu(G, U, dev(q), D, plan, x_scales=dev(s), h=h.t)
+        torch.cuda.synchronize()
+        h.check("h")
+        ref.check(f64(h.t), want([gate, up], (q, s), I, False), ht, (t, top_k, e, n, k))
+    x = activations(r, t, k, BF16)
+    codes, scales = qmm.i8_quantize(x)
+    a = qmm.i8_moe_gate_up_swiglu(G, U, x, D, plan, dtype=BF16)
+    b = qmm.i8_moe_gate_up_swiglu(G, U, codes, D, plan, x_scales=scales, dtype=BF16)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("yt", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("t,top_k", [(1, 8), (8, 2), (30, 2), (300, 4)])
+def test_a_plan_built_for_other_counts_leaves_nothing_of_the_output(t, top_k, yt):
+    """In few rows and in tiles, of one token more, of other pairs a token and of other
+    experts: every value becomes NaN, and nothing beside the output changes."""
+    say("i8 grouped foreign plans", t, top_k, yt)
+    r = np.random.default_rng([27, t, top_k])
+    e, n, k = 4, 70, 64
+    w, ws = map(dev, experts(r, e, n, k))
+    a = activations(r, t, k, F16)
+    I = dev(some_ids(r, t, top_k, e, "any"))
+    for J, other in ((some_ids(r, t + 1, top_k, e, "any"), e), (some_ids(r, t, top_k + 1, e, "any"), e), (some_ids(r, t, top_k, e, "any"), e + 5)):
+        plan = qmm.moe_route(dev(J), other)
+        for x, xs in ((a, None), qmm.i8_quantize(a)):
+            for per_pair in (False, True):
+                rows, scales = x, xs
+                if per_pair:
+                    rows = x.repeat_interleave(top_k, 0)
+                    scales = None if xs is None else xs.repeat_interleave(top_k)
+                y = Guarded((t * top_k, n), yt)
+                y.t.fill_(1)
+                qmm.i8_gemm_grouped(w, ws, rows, I, plan, per_pair, a_scales=scales, y=y.t)
+                torch.cuda.synchronize()
+                y.check("y")
+                assert y.t.isnan().all()
+            h = Guarded((t * top_k, n), yt)
+            h.t.fill_(1)
+            qmm.i8_moe_gate_up_swiglu((w, ws), (w, ws), x, I, plan, x_scales=xs, h=h.t)
+            torch.cuda.synchronize()
+            h.check("h")
+            assert h.t.isnan().all()
