@@ -39,10 +39,14 @@ size_t i8_few_lds(int rows, int k) {
   return kI8FewHead + (held > sums ? held : sums);
 }
 
-// Waves that share 16 columns: enough for about 4096 waves in all.  us of a call
-// with 8 / 4 / 2 (graph, cold weights, fp16 x): one row, 9728 x 2560: 9.6 / 12.6 /
-// 11.8; one row, 151936 x 1024: - / 34.7 / 32.0 (1: 39.8); 4 rows, 6144 x 2560: 10.3 /
-// 10.7 / 13.6.  Of codes 8 is best (16 rows, 9728 x 2560: 16.4 / 21.9 / 19.8).
+// Waves that share 16 columns: 8 with few blocks, 2 with many.  us of a call with
+// 8 / 4 / 2 (graph, weights from memory, fp16 x, one row): 9728 x 2560 (608 blocks): 9.3 /
+// 12.2 / 11.8; 16384 x 1024 (1024): 8.0 / 7.4 / 6.4; 20480 x 2560 (1280): 13.4 / 17.2 /
+// 18.7; 32752 x 1024 (2047): 12.9 / 10.4 / 9.3; 32752 x 2560: 19.0 / 21.9 / 20.3; 40960 x
+// 1024 (2560): 15.0 / 11.9 / 11.5; 151936 x 1024 (9496): - / 34.7 / 32.0 (1: 39.8).  In
+// between it is k that decides (short rows want 2, long ones 8) and 4 is seldom best of
+// all but never far behind: up to 28 % behind 8 and 19 % behind 2.  4 rows, 6144 x 2560:
+// 8.4 / 9.0 / 11.9.  Of codes 8 is best (16 rows, 9728 x 2560: 10.2 / 15.7 / 13.5).
 inline int i8_few_kw(long blocks, bool codes) {
   return codes || blocks < 1024 ? 8 : blocks < 2048 ? 4 : 2;
 }
@@ -102,7 +106,7 @@ __device__ __forceinline__ void i8_few(const I8FewTile& t, char* lds, XRow x_row
   }
   const int row = li < t.rows ? li : t.rows - 1;
   // codes of x are read along their rows and turned into operands by way of LDS
-  // (16 rows, 9728 x 2560, rounding included: 16.4 us; straight into the operands 18.6)
+  // (16 rows, 9728 x 2560: 2.2 us less than straight into the operands)
   constexpr int XS = U * 64 + 16;  // bytes of a row of a batch
   char* held = body + wave * 16 * XS;
   uint32_t xo[STAGED ? 1 : U];

@@ -204,15 +204,18 @@ static hipError_t launch_shape(I8GemmArgs& g, int splits, hipStream_t st) {
 
 // Tile shapes and what a round of their tiles costs on a full chip (of shapes that a
 // CU holds several of: of all it holds): `fixed` us and `step` us for 128 bytes of k.
-// Measured, k in one part (m x n x k, us of a call of codes, graph, cold weights):
+// Measured, k in one part (m x n x k, us of a call of codes, graph, weights from memory;
+// in brackets from the last-level cache, which holds 256 MB):
 //   shape      64x1024x4096  512x2560x4096  512x9728x2560  1024x2560x9728  2048x2560x9728  2048x9728x2560  16384x2560x9728
-//   64 x 64            11.2           13.9           31.7            58.5            94.7           101.1              649
-//   64 x 128           13.6           14.1           38.2            67.3           102.7           121.9              632
-//   128 x 128          18.3           18.5           35.5            47.3            92.9            86.3              485
-//   128 x 192          24.2           24.9           23.8            57.0            67.0            83.2              465
-//   256 x 192          37.9           39.1           35.0            93.7            93.8            72.0              420
-//   256 x 256          44.3           48.5           39.8           110.9           111.0            79.2              385
-//   256 x 320          56.8           57.9           44.9           129.5           130.2            58.2              346
+//   64 x 64     15.2 (11.2)    19.6 (14.5)           31.7            58.5            94.7           101.1              649
+//   64 x 128    17.6 (13.7)    16.9 (14.5)           38.2            67.3           102.7           121.9              632
+//   128 x 128   20.0 (18.2)    21.3 (18.7)           35.5            47.3            92.9            86.3              485
+//   128 x 192   25.0 (24.1)    26.4 (25.0)           23.8            57.0            67.0            83.2              465
+//   256 x 192   40.5 (37.8)    42.0 (39.3)           35.0            93.7            93.8            72.0              420
+//   256 x 256   45.5 (44.1)    50.6 (47.9)           39.8           110.9           111.0            79.2              385
+//   256 x 320   58.5 (56.9)    60.1 (58.0)           44.9           129.5           130.2            58.2              346
+// The model takes the fastest of each column but one (512 x 2560 x 4096 from memory), and
+// overstates large tiles where there are few of them: 256 x 320, 64 x 1024 x 4096: 76 us.
 // A larger tile moves fewer bytes for its products; which one is best is mostly a
 // matter of how evenly its tiles fall on the 256 CUs.
 struct I8Choice {
@@ -228,7 +231,7 @@ constexpr int kI8Shapes = sizeof(kI8Choices) / sizeof(kI8Choices[0]);
 // Parts of k, where there are too few tiles for the CUs: the sums of each part go
 // through memory (int32, so that their order does not matter) and a second launch adds
 // them up: `kI8SumFixed` us and 8 bytes an output and part at 4 TB/s.  64 x 2560 x
-// 9728: 31.1 us in one part, 14.5 in six; 64 x 1024 x 4096: 11.2, 9.0 in four.
+// 9728: 31.1 us in one part, 14.5 in six; 64 x 1024 x 4096: 15.2, 10.2 in four.
 constexpr float kI8SumFixed = 4.0f, kI8SumRate = 4.0e6f;
 constexpr long kI8SumMost = 64l << 20;  // bytes of sums
 
@@ -319,15 +322,17 @@ static hipError_t launch_few(I8GemmArgs& g, hipStream_t st) {
 }
 
 // How a call runs, decided once: `staged` (the product rounds x itself) goes with
-// few rows only.  us of a call, rounding of fp16 x included (graph, cold weights):
+// few rows only.  us of a call, rounding of fp16 x included (graph, weights from memory):
 //   rows x n x k          rounded in the product   few rows, codes   tiles of 64 x 64
-//    1 x 9728 x 2560                 9.6                 14.2              17.0
-//    4 x 9728 x 2560                12.2                 14.6              17.3
-//    4 x 2560 x 9728                   -                 17.2              36.8
-//    8 x 1024 x 1024                 4.4                  6.7               8.4
-//    8 x 151936 x 1024              34.6                 41.4              38.2
-//   16 x 9728 x 2560                   -                 16.4              17.5
-//   16 x 151936 x 1024                 -                 46.9              39.4
+//    1 x 9728 x 2560                 9.5                 11.1              14.0
+//    4 x 9728 x 2560                10.0                 11.7              14.3
+//    4 x 2560 x 9728                   -                 15.4              17.5 (k whole: 34.7)
+//    8 x 1024 x 1024                 5.3                  6.8               9.2
+//    8 x 151936 x 1024              32.6                 39.0              37.7
+//   16 x 9728 x 2560                   -                 13.6              14.6
+//   16 x 16384 x 1024                  -                  9.7              10.2
+//   16 x 32768 x 1024                  -                 13.7              12.6
+//   16 x 151936 x 1024                 -                 40.9              38.4
 // (The workspace's size follows from it: it looks at m, n, k and x's type alone.)
 I8Way i8_gemm_way(const I8GemmArgs& g) {
   I8Way way{false, false, -1, 1};

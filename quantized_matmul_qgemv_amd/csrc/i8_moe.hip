@@ -182,8 +182,10 @@ static hipError_t launch_moe_few_type(I8MoeArgs& g, hipStream_t st) {
 }
 
 // How a call runs, decided once: few rows, where no row tile can have more than 16
-// (`staged`: not more than a workgroup rounds for itself), or tiles.  One token, 8 of
-// 128 experts, gate and up of 768 x 2048: 9.7 us, as codes 13.4, in tiles 29.6.
+// (`staged`: not more than a workgroup rounds for itself), or tiles.  us of a call, 128
+// experts, weights from memory, fp16 rows: rounded in the product / before it / tiles
+//   one token, 8 pairs:   gate and up of 768 x 2048   9.7 / 12.8 / 23.3   down    7.1 /  9.4 / 11.5
+//   two tokens, 16 pairs:                               - / 16.3 / 24.4   down      - / 13.0 / 12.5
 I8Way i8_moe_way(const I8MoeArgs& g) {
   const long pairs = (long)g.t * g.top_k;
   I8Way way{pairs <= kI8FewRows, false, g.plan_rows >= 128 ? 1 : 0, 1};
